@@ -57,7 +57,8 @@ typedef enum {
     GDN_ERR_WORKSPACE = 6, /* workspace missing or smaller than required */
     GDN_ERR_CUDA = 7,      /* a CUDA launch or runtime call failed */
     GDN_ERR_TIMEOUT = 8,   /* a bounded device-side wait gave up */
-    GDN_ERR_BOUNDS = 9     /* a device-side index check failed (library built with GDN_DEBUG_CHECKS) */
+    GDN_ERR_BOUNDS = 9,    /* a device-side index check failed (library built with GDN_DEBUG_CHECKS) */
+    GDN_ERR_PAGES = 10     /* a cache slot, page number or cached length is outside the cache */
 } gdn_status;
 
 typedef enum { GDN_F32 = 0, GDN_BF16 = 1 } gdn_dtype;
@@ -266,6 +267,66 @@ gdn_status gdn_proj_w8(const void *x, const int8_t *w, const float *scale, int T
 gdn_status gdn_attn_fwd(const void *q, const void *k, const void *v, const int32_t *cu_seqlens, int N,
                         int T_tot, int H, int d, int max_len, float scale, gdn_dtype dtype, void *o,
                         void *workspace, size_t ws_bytes, void *stream);
+
+/*
+ * The attention layers in serving: gdn_qk_norm_rope turns the projection's q, k, v into the
+ * attention's inputs and fills the layer's cache, gdn_attn_prefill attends over whole prompts and
+ * gdn_attn_decode attends from one new token per sequence over the cache. The pages name the hybrid
+ * backbone's attention layers (page 1, abstract) and print none of this; these are the plain forms.
+ *   - Query heads come in groups: Hq is a multiple of Hkv and query head h reads key head
+ *     h / (Hq / Hkv).
+ *   - q [T][Hq][d] and k, v [T][Hkv][d] have contiguous tokens (heads d elements apart) whose distance
+ *     is given as a stride in elements, a multiple of 16 bytes: Hq d for a tensor of its own, Hq d +
+ *     2 Hkv d for a slice of a fused projection's output. Outputs q_out, k_out, o are contiguous.
+ *   - The cache of a layer is k_cache, v_cache [num_pages][Hkv][page_size][d], page_size 16, 32, 64 or
+ *     128; slot s is place s % page_size of page s / page_size. num_pages page_size <= 2^31 - 1.
+ *   - workspace: the error word (and what the entry point says), as elsewhere; gdn_chunk_fwd_check
+ *     reads it. Calls that overlap on the GPU, replays of captured graphs among them, must not share
+ *     a workspace. Index arrays (int32) are 4-byte aligned.
+ */
+
+/*
+ * Norms of queries and keys for each head, the position rotation in the same pass, and the write of
+ * keys and values into the cache. For every token t and head row x of q or k (d elements):
+ *     x^ = x w / sqrt(mean(x^2) + eps)
+ *     y_i = x^_i cos a_i - x^_{i+rot/2} sin a_i,  y_{i+rot/2} = x^_{i+rot/2} cos a_i + x^_i sin a_i
+ *         for i < rot/2, with a_i = positions[t] base^(-2i/rot);   y_i = x^_i for i >= rot
+ * in fp32 (angles in fp64 turns, so that far positions keep their phase), rounded once.
+ *   q, k, v   dtype, with strides; v is read only with slots
+ *   wq, wk    [d] fp32 norm weights, or NULL for ones; eps >= 0
+ *   positions [T] int32 (may be NULL when rot is 0)
+ *   rot       0 (no rotation) or a power of two from 16 to d; base > 1
+ *   q_out     [T][Hq][d] dtype; may be q itself if q is contiguous
+ *   k_out     [T][Hkv][d] dtype, or NULL; may be k itself if k is contiguous
+ *   slots     [T] int32 or NULL: token t's rotated keys and its values also go to that slot of k_cache
+ *             and v_cache; -1 leaves the token out of the cache. Any other slot outside the cache
+ *             leaves it out too and is reported as GDN_ERR_PAGES. If two tokens name the same slot,
+ *             its contents are one of theirs or a mixture. Slots that no token names keep what they hold.
+ * d is 64 or 128, dtype GDN_F32 or GDN_BF16 (q, k, v, the outputs and the cache alike). One kernel.
+ */
+gdn_status gdn_qk_norm_rope(const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v,
+                            int64_t v_stride, const float *wq, const float *wk, float eps, const int32_t *positions,
+                            int T, int Hq, int Hkv, int d, int rot, double base, gdn_dtype dtype, void *q_out,
+                            void *k_out, void *k_cache, void *v_cache, const int32_t *slots, int num_pages,
+                            int page_size, void *workspace, size_t ws_bytes, void *stream);
+
+/*
+ * Causal attention over whole prompts with grouped heads:
+ *     o_t = sum_{j <= t} softmax_j(scale * q_t . k_j) v_j
+ * over the keys of the same sequence, as gdn_attn_fwd, for Hq / Hkv from 1 to 16, d 64 or 128, and
+ * strided q, k, v; o [T_tot][Hq][d] must not alias them. dtype must be GDN_BF16.
+ *   cu_seqlens [N+1] int32 on the device, or NULL for N equal sequences; max_len bounds the
+ *     sequences' lengths (ignored when cu_seqlens is NULL). Empty sequences are fine. If cu_seqlens is
+ *     malformed or a sequence is longer than max_len nothing is written and GDN_ERR_SEQLENS recorded.
+ *   scale > 0, or <= 0 for 1 / sqrt(d)
+ *   workspace, ws_bytes: >= 256 bytes (also GDN_ERR_TIMEOUT if a bounded wait gave up).
+ * The scores stay in tensor memory. A sequence's outputs depend on its own rows alone, whatever values
+ * (NaN included) its neighbours in the pack hold. One kernel.
+ */
+gdn_status gdn_attn_prefill(const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v,
+                            int64_t v_stride, const int32_t *cu_seqlens, int N, int T_tot, int Hq, int Hkv, int d,
+                            int max_len, float scale, gdn_dtype dtype, void *o, void *workspace, size_t ws_bytes,
+                            void *stream);
 
 /*
  * The sequential (token-by-token) scan on the GPU: the same result as

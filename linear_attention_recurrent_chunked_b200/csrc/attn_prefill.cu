@@ -1,0 +1,407 @@
+// Causal attention with grouped heads over packed prompts, and the same kernel without the mask over
+// a cached prefix that a whole decode batch shares, on the sm_100a tensor cores.
+//
+//     o_t = sum_{j <= t} softmax_j(scale q_t . k_j) v_j,     key head = query head / G, G = Hq / Hkv
+//
+// A tile of 128 query rows packs P = floor(128 / G) consecutive positions times the G query heads of
+// one key head, position-major, which is the order in which one TMA box {64 columns, G heads,
+// P positions} lands. All rows of a tile then share their key and value tiles whatever G is, and a
+// tile's causal edge is P positions long. Per key tile of 128 keys
+//
+//     S = Q K^T (tensor memory)  ->  P = 2^(S c - m) (bf16, over S)  ->  O += P V (tensor memory)
+//
+// with c = scale log2(e) and m a running row maximum that moves only when the true one has grown by
+// more than 8, so P <= 2^8 and O and the row sum l are seldom rescaled; o = O / l. P is rounded to
+// bf16 for the tensor core (at most 2^-8 of each weight); l sums the unrounded weights in fp32.
+//
+// One CTA holds two tiles (256 rows): while the softmax warps of one turn its S into P, the tensor
+// core works on the other. Roles:
+//   softmax  (2 x 4 warps)  one query row per thread
+//   loader   (1 warp)       TMA: Q once, then K and V tiles through one ring
+//   MMA      (1 warp)       per key tile and query tile: O += P V, then the next S once that product
+//                           has read P (a later tcgen05.mma is not ordered after an earlier one's
+//                           tensor-memory operand reads)
+// Key tiles are counted from the sequence's start (or the prefix split's), so a tile may reach past
+// the end into another sequence's rows or stale cache slots; their weights are zero, and their V rows
+// are overwritten with zeros in shared memory before the product, so that a NaN there stays there.
+// Every wait is bounded in time; a timeout sets the error word and all roles leave their loops.
+#include <math.h>
+
+#include <algorithm>
+
+#include "attn_common.cuh"
+#include "chunk_common.cuh"
+#include "kernels.h"
+
+namespace gdn {
+namespace {
+
+using attn::Ctl;
+using attn::wait_bar;
+using attn::wait_bar_w;
+using bf16 = __nv_bfloat16;
+
+constexpr int TQ = 128, TK = 128;
+constexpr float kRescale = 8.f;  // log2 units
+constexpr int NTHREADS = 320;
+constexpr int W_LOAD = 8, W_MMA = 9;
+
+template <int D>
+struct Layout {
+    static constexpr uint32_t TILE = 128 * D * 2;      // D / 64 column blocks of 128 rows x 128 bytes
+    static constexpr int NST = D == 128 ? 5 : 8;       // K and V tiles in the ring
+    static constexpr uint32_t OFF_Q = 0, OFF_KV = 2 * TILE, OFF_BAR = OFF_KV + NST * TILE;
+    // barriers: Q landed, ring full / empty, and per query tile: S complete, P written, O += P V done
+    static constexpr int QFULL = 0, FULL = 1, EMPTY = FULL + NST, SFULL = EMPTY + NST, PREADY = SFULL + 2,
+                         PVD = PREADY + 2, FIN = PVD + 2, NBAR = FIN + 1;
+    static constexpr uint32_t OFF_CTL = OFF_BAR + 8 * NBAR;
+    static constexpr uint32_t SMEM = OFF_CTL + 16 + 1024;
+    static constexpr uint32_t TM_S = 0, TM_O = 256;    // S (and P over it) of tile u at u * 128, O at 256 + u * D
+};
+
+// What a CTA works on: query positions [pos0, pos0 + 2 P) of `rows` rows from token `t0`, key tiles
+// [0, nk[u]) of each query tile, keys from k0 on, `keys` of them there.
+struct Item {
+    int t0, len, pos0, head, k0, keys, nk0, nk1, split;
+};
+
+// cu_seqlens malformed: the same answer from every thread of the CTA.
+__device__ __forceinline__ bool seqlens_bad(const AttnPrefill &a) {
+    bool bad = false;
+    for (int n = threadIdx.x; n < a.N; n += NTHREADS) {
+        const int x = a.cu[n], y = a.cu[n + 1];
+        bad |= y < x || y - x > a.max_len || x < 0 || y > a.T_tot;
+    }
+    if (threadIdx.x == 0) bad |= a.cu[0] != 0 || a.cu[a.N] != a.T_tot;
+    return __syncthreads_or(bad);
+}
+
+template <int D, bool PREFIX>
+__global__ void __launch_bounds__(NTHREADS, 1)
+    k_attn_prefill(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                   const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ AttnPrefill a) {
+    using L = Layout<D>;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw_base = tc::smem_u32(smem_raw);
+    uint8_t *smem = smem_raw + ((1024u - (raw_base & 1023u)) & 1023u);
+    const uint32_t sb = tc::smem_u32(smem);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int P = a.P;
+
+    Item it;
+    if (PREFIX) {
+        const int b = blockIdx.x, rb = b / (a.Hkv * a.splits), rem = b - rb * a.Hkv * a.splits;
+        it.head = rem / a.splits;
+        it.split = rem - it.head * a.splits;
+        it.t0 = 0;
+        it.len = a.T_tot;
+        it.pos0 = rb * 2 * P;
+        // key tiles spread over the splits as evenly as they go
+        const int tiles = (a.prefix_len + TK - 1) / TK;
+        const int k0 = (int)((int64_t)tiles * it.split / a.splits), k1 = (int)((int64_t)tiles * (it.split + 1) / a.splits);
+        it.k0 = k0 * TK;
+        it.keys = a.prefix_len - it.k0;
+        it.nk0 = k1 - k0;
+        it.nk1 = it.pos0 + P < it.len ? it.nk0 : 0;
+    } else {
+        // blocks are numbered so that the query tiles with the most key tiles come first
+        const int per = a.Hkv * a.N, r = blockIdx.x / per, rem = blockIdx.x - r * per;
+        it.head = rem / a.N;
+        const int n = rem - it.head * a.N;
+        it.split = 0;
+        if (a.cu) {
+            const bool bad = seqlens_bad(a);
+            if (blockIdx.x == 0 && tid == 0) *a.err = bad ? ERRBIT_SEQLENS : 0u;
+            if (bad) return;
+        } else if (blockIdx.x == 0 && tid == 0) {
+            *a.err = 0u;
+        }
+        int t1;
+        seq_bounds(a.cu, n, a.N, a.T_tot, it.t0, t1);
+        it.len = t1 - it.t0;
+        it.pos0 = (a.blocks - 1 - r) * 2 * P;
+        if (it.pos0 >= it.len) return;
+        it.k0 = it.t0;
+        it.keys = it.len;
+        const int e0 = min(it.pos0 + P, it.len), e1 = min(it.pos0 + 2 * P, it.len);
+        it.nk0 = (e0 + TK - 1) / TK;
+        it.nk1 = e1 > it.pos0 + P ? (e1 + TK - 1) / TK : 0;
+    }
+    const int nk = max(it.nk0, it.nk1);
+
+    uint64_t *bar = reinterpret_cast<uint64_t *>(smem + L::OFF_BAR);
+    Ctl *ctl = reinterpret_cast<Ctl *>(smem + L::OFF_CTL);
+    if (warp == W_MMA) tc::tmem_alloc(&ctl->tmem, 512);
+    if (tid == W_LOAD * 32) {
+        for (int i = 0; i < L::NBAR; ++i) tc::mbar_init(&bar[i], (i == L::PREADY || i == L::PREADY + 1) ? 128u : 1u);
+        ctl->abort = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    const uint32_t tm = ctl->tmem;
+
+    if (warp == W_LOAD) {
+        if (lane == 0) {
+            const uint32_t bytes = (uint32_t)(a.G * P) * 128u * (D / 64);
+            tc::mbar_arrive_expect_tx(&bar[L::QFULL], it.nk1 ? 2 * bytes : bytes);
+            for (int u = 0; u < (it.nk1 ? 2 : 1); ++u)
+#pragma unroll
+                for (int hf = 0; hf < D / 64; ++hf)
+                    tc::tma_load_3d(sb + L::OFF_Q + u * L::TILE + hf * 16384, &tm_q, &bar[L::QFULL], 64 * hf, it.head * a.G,
+                                    it.t0 + it.pos0 + u * P);
+        }
+        __syncwarp();
+        // paged: lane i brings box i of a tile, whose page number it fetched a tile ahead
+        const int boxes = PREFIX ? TK >> a.page_log : 1, rows = TK / boxes;
+        const int npages = PREFIX ? (a.prefix_len + (1 << a.page_log) - 1) >> a.page_log : 0;
+        auto page_of = [&](int j) {
+            const int i = ((it.k0 + j * TK) >> a.page_log) + lane;
+            int p = a.num_pages;  // beyond the tensor: reads as zero
+            if (lane < boxes && i < npages) {
+                const int x = a.pages[i];
+                if (x >= 0 && x < a.num_pages) p = x;
+            }
+            return p;
+        };
+        int page = PREFIX ? page_of(0) : 0;
+        bool ok = true;
+        int c = 0;  // tiles brought
+        for (int j = 0; ok && j < nk; ++j) {
+            for (int kv = 0; kv < 2; ++kv, ++c) {
+                const int st = c % L::NST;
+                if (c >= L::NST && !(ok = wait_bar_w(&bar[L::EMPTY + st], (uint32_t)((c / L::NST - 1) & 1), ctl, a.err))) break;
+                if (lane == 0) tc::mbar_arrive_expect_tx(&bar[L::FULL + st], L::TILE);
+                __syncwarp();
+                const CUtensorMap *map = kv ? &tm_v : &tm_k;
+                const uint32_t dst = sb + L::OFF_KV + st * L::TILE + lane * rows * 128;
+                if (lane < boxes) {
+#pragma unroll
+                    for (int hf = 0; hf < D / 64; ++hf) {
+                        if (PREFIX)
+                            tc::tma_load_3d(dst + hf * 16384, map, &bar[L::FULL + st], 64 * hf, 0, page * a.Hkv + it.head);
+                        else
+                            tc::tma_load_3d(dst + hf * 16384, map, &bar[L::FULL + st], 64 * hf, it.head, it.k0 + j * TK);
+                    }
+                }
+            }
+            if (PREFIX && j + 1 < nk) page = page_of(j + 1);
+        }
+        if (lane == 0) {
+            attn::drain_bar(&bar[L::QFULL], 0);
+            for (int i = std::max(c - L::NST, 0); i < c; ++i) attn::drain_bar(&bar[L::FULL + i % L::NST], (i / L::NST) & 1);
+        }
+        __syncwarp();
+    } else if (warp == W_MMA) {
+        const uint32_t id_s = tc::make_idesc_bf16(TQ, TK, 0, 0);  // Q K^T: both K-major
+        const uint32_t id_o = tc::make_idesc_bf16(TQ, D, 0, 1);   // P V: V MN-major
+        const tc::Desc dq = tc::split_desc(tc::make_desc_sw128(sb + L::OFF_Q, 16, 1024));
+        const tc::Desc dk = tc::split_desc(tc::make_desc_sw128(sb + L::OFF_KV, 16, 1024));
+        const tc::Desc dv = tc::split_desc(tc::make_desc_sw128(sb + L::OFF_KV, 16384, 1024));
+        // the ring holds K_j as tile 2 j and V_j as tile 2 j + 1
+        auto full = [&](int c) { return wait_bar_w(&bar[L::FULL + c % L::NST], (uint32_t)((c / L::NST) & 1), ctl, a.err); };
+        auto issue_s = [&](int u, int j) {
+            const uint32_t kb = (uint32_t)((2 * j) % L::NST) * L::TILE;
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+                const uint32_t off = (kk >> 2) * 16384 + (kk & 3) * 32;
+                tc::mma_bf16_off_w(tm + L::TM_S + u * 128, dq, u * L::TILE + off, dk, kb + off, id_s, kk > 0);
+            }
+            tc::mma_commit_w(&bar[L::SFULL + u]);
+        };
+        const int nku[2] = {it.nk0, it.nk1};
+        bool ok = wait_bar_w(&bar[L::QFULL], 0, ctl, a.err) && full(0);
+        if (ok) {
+            tc::fence_after_sync();
+            issue_s(0, 0);
+            if (it.nk1) issue_s(1, 0);
+            tc::mma_commit_w(&bar[L::EMPTY]);
+        }
+        for (int j = 0; ok && j < nk; ++j) {
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                if (!ok || j >= nku[u]) continue;
+                if (!(ok = wait_bar_w(&bar[L::PREADY + u], (uint32_t)(j & 1), ctl, a.err) && full(2 * j + 1))) continue;
+                tc::fence_after_sync();
+                const uint32_t vb = (uint32_t)((2 * j + 1) % L::NST) * L::TILE;
+#pragma unroll
+                for (int kk = 0; kk < TK / 16; ++kk)
+                    tc::mma_bf16_ts_off_w(tm + L::TM_O + u * D, tm + L::TM_S + u * 128 + 8 * kk, dv, vb + kk * 2048, id_o,
+                                          (j > 0 || kk > 0) ? 1u : 0u);
+                tc::mma_commit_w(&bar[L::PVD + u]);
+                if (u == 1 || j >= nku[1]) tc::mma_commit_w(&bar[L::EMPTY + (2 * j + 1) % L::NST]);
+                if (j + 1 < nku[u]) {
+                    if (!(ok = full(2 * j + 2) && wait_bar_w(&bar[L::PVD + u], (uint32_t)(j & 1), ctl, a.err))) continue;
+                    tc::fence_after_sync();
+                    issue_s(u, j + 1);
+                    if (u == 1 || j + 1 >= nku[1]) tc::mma_commit_w(&bar[L::EMPTY + (2 * j + 2) % L::NST]);
+                }
+            }
+        }
+        tc::mma_commit_w(&bar[L::FIN]);
+        if (lane == 0) attn::drain_bar(&bar[L::FIN], 0);
+        __syncwarp();
+    } else {
+        // ---------------------------------------------------------------- softmax (one query row per thread)
+        const int u = warp >> 2, r = tid & 127;
+        const uint32_t tl = tm + ((uint32_t)((warp & 3) * 32) << 16);
+        const uint32_t ts = tl + L::TM_S + u * 128, to = tl + L::TM_O + u * D;
+        const int mynk = u ? it.nk1 : it.nk0;
+        const int pos = it.pos0 + u * P + r / a.G;  // position within the sequence
+        const int first = it.pos0 + u * P;          // the tile's first position
+        const float sc = a.scale_log2;
+        float m_ref = -INFINITY, l = 0.f;
+        bool ok = true;
+        for (int j = 0; ok && j < mynk; ++j) {
+            if (!(ok = wait_bar_w(&bar[L::SFULL + u], (uint32_t)(j & 1), ctl, a.err))) break;
+            tc::fence_after_sync();
+            float s[128];
+#pragma unroll
+            for (int c0 = 0; c0 < 128; c0 += 32) {
+                float x[32];
+                tc::tmem_ld32(ts + c0, x);
+#pragma unroll
+                for (int i = 0; i < 32; ++i) s[c0 + i] = x[i];
+            }
+            // keys beyond this row's position, or beyond the prefix, are masked
+            const int lim = (PREFIX ? it.keys - 1 : pos) - j * TK;
+            if (PREFIX ? lim < TK - 1 : first - j * TK < TK - 1) {
+#pragma unroll
+                for (int i = 0; i < 128; ++i) s[i] = (i <= lim) ? s[i] : -INFINITY;
+            }
+            float pm[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) pm[i] = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < 128; ++i) pm[i & 7] = fmaxf(pm[i & 7], s[i]);
+            const float mt = fmaxf(fmaxf(fmaxf(pm[0], pm[1]), fmaxf(pm[2], pm[3])),
+                                   fmaxf(fmaxf(pm[4], pm[5]), fmaxf(pm[6], pm[7]))) * sc;
+            float alpha = 1.f;
+            const bool grow = mt > m_ref + kRescale;
+            if (grow) {
+                alpha = (m_ref == -INFINITY) ? 0.f : exp2f(m_ref - mt);
+                m_ref = mt;
+                l *= alpha;
+            }
+            if (j > 0 && __any_sync(0xffffffffu, grow)) {
+                if (!(ok = wait_bar_w(&bar[L::PVD + u], (uint32_t)((j - 1) & 1), ctl, a.err))) break;
+                tc::fence_after_sync();
+#pragma unroll 1
+                for (int c0 = 0; c0 < D; c0 += 32) {
+                    uint32_t w[32];
+                    tc::tmem_ld32_nowait(to + c0, w);
+                    tc::tmem_wait_ld(w);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) w[i] = __float_as_uint(__uint_as_float(w[i]) * alpha);
+                    tc::tmem_st32(to + c0, w);
+                }
+            }
+            float ps[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) ps[i] = 0.f;
+#pragma unroll
+            for (int c0 = 0; c0 < 128; c0 += 64) {
+                uint32_t w[32];
+#pragma unroll
+                for (int i = 0; i < 32; ++i) {
+                    const float p0 = chunk::ex2(fmaf(s[c0 + 2 * i], sc, -m_ref));
+                    const float p1 = chunk::ex2(fmaf(s[c0 + 2 * i + 1], sc, -m_ref));
+                    ps[i & 7] += p0 + p1;
+                    w[i] = tc::pack_bf16x2(p0, p1);
+                }
+                tc::tmem_st32(ts + c0 / 2, w);
+            }
+            l += ((ps[0] + ps[1]) + (ps[2] + ps[3])) + ((ps[4] + ps[5]) + (ps[6] + ps[7]));
+            if (it.keys - j * TK < TK) {
+                // rows of V beyond the sequence or the prefix: another sequence's values or stale slots
+                const int c = 2 * j + 1, st = c % L::NST;
+                if (!(ok = wait_bar_w(&bar[L::FULL + st], (uint32_t)((c / L::NST) & 1), ctl, a.err))) break;
+                if (r >= it.keys - j * TK) {
+#pragma unroll
+                    for (int hf = 0; hf < D / 64; ++hf)
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            chunk::st_shared_v4(sb + L::OFF_KV + st * L::TILE + hf * 16384 + r * 128 + i * 16, 0, 0, 0, 0);
+                }
+                tc::fence_smem_to_async();
+            }
+            tc::tmem_st_wait();
+            tc::fence_before_sync();
+            tc::mbar_arrive(&bar[L::PREADY + u]);
+        }
+        if (ok && mynk) ok = wait_bar_w(&bar[L::PVD + u], (uint32_t)((mynk - 1) & 1), ctl, a.err);
+        if (ok && mynk) {
+            tc::fence_after_sync();
+            const bool valid = r < a.G * P && pos < it.len;
+            const int64_t row = (int64_t)(it.t0 + pos) * a.Hq + it.head * a.G + r % a.G;
+            if (PREFIX) {
+                // unnormalised, with the reference maximum (log2 units) and the sum
+                const int64_t prow = (int64_t)it.split * a.T_tot * a.Hq + row;
+                if (valid) a.part_ml[prow] = make_float2(m_ref, l);
+#pragma unroll 1
+                for (int c0 = 0; c0 < D; c0 += 32) {
+                    float x[32];
+                    tc::tmem_ld32(to + c0, x);
+                    if (valid) {
+#pragma unroll
+                        for (int i = 0; i < 32; i += 4)
+                            *reinterpret_cast<float4 *>(a.part_o + prow * D + c0 + i) =
+                                make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
+                    }
+                }
+            } else {
+                const float inv = 1.f / l;
+                bf16 *dst = a.o + row * D;
+#pragma unroll 1
+                for (int c0 = 0; c0 < D; c0 += 32) {
+                    float x[32];
+                    tc::tmem_ld32(to + c0, x);
+                    if (valid) {
+#pragma unroll
+                        for (int i = 0; i < 32; i += 8)
+                            *reinterpret_cast<uint4 *>(dst + c0 + i) = make_uint4(
+                                tc::pack_bf16x2(x[i] * inv, x[i + 1] * inv), tc::pack_bf16x2(x[i + 2] * inv, x[i + 3] * inv),
+                                tc::pack_bf16x2(x[i + 4] * inv, x[i + 5] * inv), tc::pack_bf16x2(x[i + 6] * inv, x[i + 7] * inv));
+                    }
+                }
+            }
+        }
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    if (warp == W_MMA) tc::tmem_dealloc(tm, 512);
+}
+
+template <int D>
+cudaError_t launch_prompt(AttnPrefill a, cudaStream_t st, const char **stage) {
+    cudaError_t e;
+    a.P = TQ / a.G;
+    a.blocks = (a.max_len + 2 * a.P - 1) / (2 * a.P);
+    CUtensorMap tm_q, tm_k, tm_v;
+    *stage = "TMA descriptor encoding";
+    if ((e = attn::make_map(&tm_q, a.q, D, a.Hq, a.T_tot, D, a.q_stride, a.G, a.P)) != cudaSuccess) return e;
+    if ((e = attn::make_map(&tm_k, a.k, D, a.Hkv, a.T_tot, D, a.k_stride, 1, TK)) != cudaSuccess) return e;
+    if ((e = attn::make_map(&tm_v, a.v, D, a.Hkv, a.T_tot, D, a.v_stride, 1, TK)) != cudaSuccess) return e;
+    *stage = "attn_prefill";
+    auto kern = k_attn_prefill<D, false>;
+    if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Layout<D>::SMEM)) != cudaSuccess)
+        return e;
+    void *pr = prof_start("attn_prefill", st);
+    kern<<<a.blocks * a.Hkv * a.N, NTHREADS, Layout<D>::SMEM, st>>>(tm_q, tm_k, tm_v, a);
+    prof_stop(pr);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_attn_prefill(const AttnPrefill &a, int d, cudaStream_t st, const char **stage) {
+    if (a.T_tot == 0 || a.max_len == 0) {
+        // nothing to compute: only the error word (cu_seqlens must then be all zeros)
+        *stage = "error word";
+        return launch_validate_seqlens(a.cu, a.N, a.T_tot, a.err, st);
+    }
+    return d == 64 ? launch_prompt<64>(a, st, stage) : launch_prompt<128>(a, st, stage);
+}
+
+}  // namespace gdn

@@ -10,7 +10,7 @@
 namespace gdn {
 
 // Device error word layout (first 4 bytes of the chunk workspace).
-enum : uint32_t { ERRBIT_SEQLENS = 1u, ERRBIT_TIMEOUT = 2u, ERRBIT_INTERNAL = 4u, ERRBIT_BOUNDS = 8u };
+enum : uint32_t { ERRBIT_SEQLENS = 1u, ERRBIT_TIMEOUT = 2u, ERRBIT_INTERNAL = 4u, ERRBIT_BOUNDS = 8u, ERRBIT_PAGES = 16u };
 
 // Index checks of the GDN_DEBUG_CHECKS build: an index into a workspace region or an output,
 // checked against the region's size. Out of range, the error word gets ERRBIT_BOUNDS and the

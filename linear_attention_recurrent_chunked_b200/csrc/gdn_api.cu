@@ -285,6 +285,8 @@ gdn_status gdn_chunk_fwd_check(const void *workspace, size_t ws_bytes, void *str
         return fail(GDN_ERR_TIMEOUT, "a bounded device-side wait gave up");
     }
     if (word & gdn::ERRBIT_INTERNAL) return fail(GDN_ERR_CUDA, "internal: misaligned shared-memory base, nothing written");
+    if (word & gdn::ERRBIT_PAGES)
+        return fail(GDN_ERR_PAGES, "a slot, page number or cached length is outside the cache");
     if (word & gdn::ERRBIT_BOUNDS)
         return fail(GDN_ERR_BOUNDS, "a device-side index check failed (GDN_DEBUG_CHECKS build): an index into the "
                                     "workspace or an output was out of range and was redirected to 0");
@@ -409,6 +411,108 @@ gdn_status gdn_attn_fwd(const void *q, const void *k, const void *v, const int32
         static_cast<const __nv_bfloat16 *>(q), static_cast<const __nv_bfloat16 *>(k),
         static_cast<const __nv_bfloat16 *>(v), cu_seqlens, N, T_tot, H, max_len, scale,
         static_cast<__nv_bfloat16 *>(o), static_cast<uint32_t *>(workspace), static_cast<cudaStream_t>(stream), &stage);
+    if (e != cudaSuccess) return cuda_fail(e, stage);
+    return ok();
+}
+
+// Token stride of a [T][H][d] tensor whose rows may lie inside a wider one (a fused projection's
+// output): at least one token's elements, and tokens 16-byte aligned like the base.
+static bool stride_ok(int64_t stride, int T, int H, int d, int esize) {
+    return (T <= 1 || stride >= (int64_t)H * d) && stride >= 0 && (stride * esize) % 16 == 0 &&
+           (double)stride * std::max(T, 1) < 4.0e18 / esize;
+}
+static bool page_size_ok(int p) { return p == 16 || p == 32 || p == 64 || p == 128; }
+
+gdn_status gdn_qk_norm_rope(const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v,
+                            int64_t v_stride, const float *wq, const float *wk, float eps, const int32_t *positions,
+                            int T, int Hq, int Hkv, int d, int rot, double base, gdn_dtype dtype, void *q_out,
+                            void *k_out, void *k_cache, void *v_cache, const int32_t *slots, int num_pages,
+                            int page_size, void *workspace, size_t ws_bytes, void *stream) {
+    if (dtype != GDN_F32 && dtype != GDN_BF16) return fail(GDN_ERR_DTYPE, "dtype %d is not GDN_F32 or GDN_BF16", dtype);
+    if (d != 64 && d != 128) return fail(GDN_ERR_SHAPE, "head size d=%d unsupported (64 or 128)", d);
+    if (T < 0 || Hq < 1 || Hkv < 1 || Hq > 65536 || Hkv > 65536)
+        return fail(GDN_ERR_SHAPE, "T=%d Hq=%d Hkv=%d out of range", T, Hq, Hkv);
+    if (rot != 0 && (rot < 16 || rot > d || (rot & (rot - 1)) != 0))
+        return fail(GDN_ERR_SHAPE, "rot=%d unsupported (0, or a power of two from 16 to d)", rot);
+    if (rot != 0 && !(base > 1.0 && isfinite(base))) return fail(GDN_ERR_SHAPE, "base must be finite and above 1");
+    if (!(eps >= 0.f) || !isfinite(eps)) return fail(GDN_ERR_SHAPE, "eps must be finite and not negative");
+    const int es = dtype == GDN_F32 ? 4 : 2;
+    if (!stride_ok(q_stride, T, Hq, d, es) || !stride_ok(k_stride, T, Hkv, d, es) ||
+        (slots && !stride_ok(v_stride, T, Hkv, d, es)))
+        return fail(GDN_ERR_SHAPE, "token strides must cover a token's heads and be multiples of 16 bytes");
+    if (T > 0 && (!q || !k || !q_out || (rot && !positions)))
+        return fail(GDN_ERR_NULL, "q, k, q_out and (with rot) positions are required");
+    if (T > 0 && !k_out && !slots) return fail(GDN_ERR_NULL, "k_out or slots is required: the keys would go nowhere");
+    if (slots && (!v || !k_cache || !v_cache)) return fail(GDN_ERR_NULL, "slots needs v, k_cache and v_cache");
+    if (!slots && (k_cache || v_cache) && T > 0) return fail(GDN_ERR_NULL, "k_cache and v_cache need slots");
+    if (slots && (!page_size_ok(page_size) || num_pages < 1 || (int64_t)num_pages * page_size > INT32_MAX))
+        return fail(GDN_ERR_SHAPE, "num_pages=%d page_size=%d unsupported (page_size 16, 32, 64 or 128; at most 2^31-1 "
+                    "slots)", num_pages, page_size);
+    const void *ptrs[] = {q, k, slots ? v : nullptr, wq, wk, q_out, k_out, k_cache, v_cache};
+    for (const void *p : ptrs)
+        if (misaligned(p)) return fail(GDN_ERR_ALIGN, "tensor pointer %p is not 16-byte aligned", p);
+    if ((reinterpret_cast<uintptr_t>(positions) | reinterpret_cast<uintptr_t>(slots)) & 3u)
+        return fail(GDN_ERR_ALIGN, "positions and slots must be 4-byte aligned");
+    if (!workspace || ws_bytes < kErrWordBytes)
+        return fail(GDN_ERR_WORKSPACE, "workspace of at least %zu bytes (the error word) needed", kErrWordBytes);
+    if ((reinterpret_cast<uintptr_t>(workspace) & 3u) != 0) return fail(GDN_ERR_ALIGN, "workspace must be 4-byte aligned");
+    const gdn::NormRope a{q, k, v, q_stride, k_stride, v_stride, wq, wk, eps, positions, T, Hq, Hkv, rot, base,
+                          q_out, k_out, k_cache, v_cache, slots, num_pages, page_size, static_cast<uint32_t *>(workspace)};
+    const cudaError_t e = gdn::launch_norm_rope(a, d, dtype == GDN_BF16, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "qk_norm_rope launch");
+    return ok();
+}
+
+gdn_status gdn_attn_prefill(const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v,
+                            int64_t v_stride, const int32_t *cu_seqlens, int N, int T_tot, int Hq, int Hkv, int d,
+                            int max_len, float scale, gdn_dtype dtype, void *o, void *workspace, size_t ws_bytes,
+                            void *stream) {
+    if (dtype != GDN_BF16) return fail(GDN_ERR_DTYPE, "attention takes bf16 inputs only");
+    if (d != 64 && d != 128) return fail(GDN_ERR_SHAPE, "head size d=%d unsupported (64 or 128)", d);
+    if (N < 1 || T_tot < 0 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || Hq / Hkv > 16)
+        return fail(GDN_ERR_SHAPE, "N=%d T=%d Hq=%d Hkv=%d unsupported (Hq a multiple of Hkv, at most 16 times it)", N,
+                    T_tot, Hq, Hkv);
+    if (!cu_seqlens && T_tot % N != 0)
+        return fail(GDN_ERR_SEQLENS, "cu_seqlens is NULL and T_tot=%d is not a multiple of N=%d", T_tot, N);
+    if (!cu_seqlens) max_len = T_tot / N;
+    if (max_len < 0 || max_len > T_tot || (int64_t)max_len * N < T_tot)
+        return fail(GDN_ERR_SHAPE, "max_len=%d cannot bound %d sequences of %d tokens together", max_len, N, T_tot);
+    if (!stride_ok(q_stride, T_tot, Hq, d, 2) || !stride_ok(k_stride, T_tot, Hkv, d, 2) ||
+        !stride_ok(v_stride, T_tot, Hkv, d, 2))
+        return fail(GDN_ERR_SHAPE, "token strides must cover a token's heads and be multiples of 16 bytes");
+    // TMA strides are below 2^40 bytes; the grid has a block per query tile pair, key head and sequence
+    const int64_t pos = 2 * (128 / (Hq / Hkv));
+    if (std::max({q_stride, k_stride, v_stride}) >= ((int64_t)1 << 39) ||
+        (double)((max_len + pos - 1) / pos) * Hkv * N >= 2.0e9)
+        return fail(GDN_ERR_SHAPE, "sizes overflow");
+    if (T_tot > 0 && (!q || !k || !v || !o)) return fail(GDN_ERR_NULL, "q, k, v and o are required");
+    const void *ptrs[] = {q, k, v, o};
+    for (const void *p : ptrs)
+        if (misaligned(p)) return fail(GDN_ERR_ALIGN, "pointer %p is not 16-byte aligned", p);
+    if ((reinterpret_cast<uintptr_t>(cu_seqlens) & 3u) != 0) return fail(GDN_ERR_ALIGN, "cu_seqlens must be 4-byte aligned");
+    if (!workspace || ws_bytes < kErrWordBytes)
+        return fail(GDN_ERR_WORKSPACE, "workspace of at least %zu bytes (the error word) needed", kErrWordBytes);
+    if ((reinterpret_cast<uintptr_t>(workspace) & 3u) != 0) return fail(GDN_ERR_ALIGN, "workspace must be 4-byte aligned");
+    if (!(scale > 0.f)) scale = 1.f / sqrtf((float)d);
+    gdn::AttnPrefill a{};
+    a.q = static_cast<const __nv_bfloat16 *>(q);
+    a.k = static_cast<const __nv_bfloat16 *>(k);
+    a.v = static_cast<const __nv_bfloat16 *>(v);
+    a.q_stride = q_stride;
+    a.k_stride = k_stride;
+    a.v_stride = v_stride;
+    a.cu = cu_seqlens;
+    a.N = N;
+    a.T_tot = T_tot;
+    a.max_len = max_len;
+    a.Hq = Hq;
+    a.Hkv = Hkv;
+    a.G = Hq / Hkv;
+    a.scale_log2 = scale * 1.4426950408889634f;
+    a.o = static_cast<__nv_bfloat16 *>(o);
+    a.err = static_cast<uint32_t *>(workspace);
+    const char *stage = "";
+    const cudaError_t e = gdn::launch_attn_prefill(a, d, static_cast<cudaStream_t>(stream), &stage);
     if (e != cudaSuccess) return cuda_fail(e, stage);
     return ok();
 }

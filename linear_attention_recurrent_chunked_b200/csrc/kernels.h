@@ -61,6 +61,44 @@ cudaError_t launch_attn_fwd(const __nv_bfloat16 *q, const __nv_bfloat16 *k, cons
                             const int32_t *cu, int N, int T_tot, int H, int max_len, float scale, __nv_bfloat16 *o,
                             uint32_t *err, cudaStream_t st, const char **stage);
 
+// Norms of queries and keys per head, the rotation, and the write into the cache's pages (see
+// gdn_qk_norm_rope): q, k, v rows of a token contiguous, tokens `*_stride` elements apart.
+struct NormRope {
+    const void *q, *k, *v;  // v used with slots only
+    int64_t q_stride, k_stride, v_stride;
+    const float *wq, *wk;  // [d], or NULL: ones
+    float eps;
+    const int32_t *positions;  // [T]
+    int T, Hq, Hkv, rot;
+    double base;
+    void *q_out, *k_out;        // k_out may be NULL
+    void *k_cache, *v_cache;    // [num_pages][Hkv][page_size][d], used with slots only
+    const int32_t *slots;       // [T] or NULL
+    int num_pages, page_size;   // page_size a power of two
+    uint32_t *err;
+};
+cudaError_t launch_norm_rope(const NormRope &a, int d, bool bf16, cudaStream_t st);
+
+// Causal attention with grouped heads over packed prompts (see gdn_attn_prefill), and the part of
+// gdn_attn_decode over the prefix that a batch shares. The fields after `err` are the latter's; for it
+// q is [B][Hq][d] with T_tot = B, and k, v are the cache.
+struct AttnPrefill {
+    const __nv_bfloat16 *q, *k, *v;
+    int64_t q_stride, k_stride, v_stride;  // elements from one token to the next
+    const int32_t *cu;
+    int N, T_tot, max_len;
+    int Hq, Hkv, G;
+    float scale_log2;  // scale * log2(e)
+    __nv_bfloat16 *o;
+    uint32_t *err;
+    const int32_t *pages;
+    int num_pages, page_log, prefix_len, splits;
+    float *part_o;    // [splits][B][Hq][d] unnormalised
+    float2 *part_ml;  // [splits][B][Hq] reference maximum (log2 units) and sum
+    int P, blocks;    // set by the launcher: positions per query tile, query tile pairs of the longest sequence
+};
+cudaError_t launch_attn_prefill(const AttnPrefill &a, int d, cudaStream_t st, const char **stage);
+
 // Failure injection for tests (set by gdn_debug_inject; off by default): the pipelined path's
 // first segment of head 0 withholds its end-state flag, and waits for flags give up after
 // flag_wait_ns (0 = the normal bound) instead of hanging.

@@ -23,10 +23,11 @@ GDN_F32, GDN_BF16 = 0, 1
 _DTYPE = {torch.float32: GDN_F32, torch.bfloat16: GDN_BF16}
 STATUS = {0: "GDN_OK", 1: "GDN_ERR_NULL", 2: "GDN_ERR_SHAPE", 3: "GDN_ERR_DTYPE", 4: "GDN_ERR_ALIGN",
           5: "GDN_ERR_SEQLENS", 6: "GDN_ERR_WORKSPACE", 7: "GDN_ERR_CUDA", 8: "GDN_ERR_TIMEOUT",
-          9: "GDN_ERR_BOUNDS"}
+          9: "GDN_ERR_BOUNDS", 10: "GDN_ERR_PAGES"}
 
 # Every symbol include/gdn.h declares, with its ctypes signature.
 _VP, _SZ, _I = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int
+_I64, _F32, _F64 = ctypes.c_int64, ctypes.c_float, ctypes.c_double
 SIGNATURES = {
     "gdn_version": (_I, []),
     "gdn_last_error": (ctypes.c_char_p, []),
@@ -36,6 +37,10 @@ SIGNATURES = {
     "gdn_decode_step_raw": (_I, [_VP, _VP, _VP, _VP, _VP, _VP, _I, _I, _I, _I, _I, _VP, _VP]),
     "gdn_chunk_fwd_check": (_I, [_VP, _SZ, _VP]),
     "gdn_attn_fwd": (_I, [_VP, _VP, _VP, _VP, _I, _I, _I, _I, _I, ctypes.c_float, _I, _VP, _VP, _SZ, _VP]),
+    "gdn_qk_norm_rope": (_I, [_VP, _I64, _VP, _I64, _VP, _I64, _VP, _VP, _F32, _VP, _I, _I, _I, _I, _I, _F64, _I, _VP,
+                              _VP, _VP, _VP, _VP, _I, _I, _VP, _SZ, _VP]),
+    "gdn_attn_prefill": (_I, [_VP, _I64, _VP, _I64, _VP, _I64, _VP, _I, _I, _I, _I, _I, _I, _F32, _I, _VP, _VP, _SZ,
+                              _VP]),
     "gdn_proj_w8": (_I, [_VP, _VP, _VP, _I, _I, _I, _I, _I, _VP, _VP, _VP, _VP, _VP, _VP, _SZ, _VP]),
     "gdn_decode_step": (_I, [_VP, _VP, _VP, _VP, _VP, _VP, _I, _I, _I, _I, _I, _VP, _VP]),
     "gdn_seq_scan": (_I, [_VP, _VP, _VP, _VP, _VP, _VP, _VP, _I, _I, _I, _I, _I, _I, _VP, _VP, _VP]),
@@ -85,6 +90,32 @@ def _ptr(t: Optional[torch.Tensor]):
 
 def _stream() -> ctypes.c_void_p:
     return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+
+
+def _at(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
+def _stream_of(device) -> int:
+    return torch.cuda.current_stream(device).cuda_stream
+
+
+class _Nothing:
+    def __enter__(self):
+        return None
+
+    def __exit__(self, *exc):
+        return False
+
+
+_NOTHING = _Nothing()
+
+
+def _on(device):
+    """Makes the tensors' device the current one for a call, where it is not."""
+    if device.type != "cuda":
+        raise GdnError(1, "tensors must be on a CUDA device (no CPU path)")
+    return _NOTHING if device.index == torch.cuda.current_device() else torch.cuda.device(device)
 
 
 def _need_cuda(*ts):
@@ -225,6 +256,142 @@ def attn_fwd(q, k, v, cu_seqlens=None, N: Optional[int] = None, max_len: Optiona
                             _DTYPE.get(q.dtype, 99), _ptr(o), _ptr(ws), ws.numel(), _stream()))
     if check:
         _check(lib.gdn_chunk_fwd_check(_ptr(ws), ws.numel(), _stream()))
+    return o
+
+
+def _heads(name, t, device, dtype, H=None, d=None):
+    """Token stride of a [T, H, d] tensor whose tokens are contiguous (the heads of one token may be a
+    slice of a wider row); raises unless it is one, on `device` and of type `dtype`."""
+    if t.dim() != 3 or (H is not None and t.shape[1] != H) or (d is not None and t.shape[2] != d):
+        raise GdnError(2, "%s has shape %s" % (name, tuple(t.shape)))
+    if t.dtype != dtype:
+        raise GdnError(3, "%s is %s, not %s" % (name, t.dtype, dtype))
+    if t.device != device or not t.is_cuda:
+        raise GdnError(1, "%s is on %s (all tensors must be on one CUDA device)" % (name, t.device))
+    st = t.stride()
+    if t.numel() and ((st[2] != 1 and t.shape[2] != 1) or (st[1] != t.shape[2] and t.shape[1] != 1)):
+        raise GdnError(2, "%s: the heads of a token must be contiguous" % name)
+    return st[0] if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+
+
+def _flat(name, t, device, dtype, shape):
+    """Checks a contiguous tensor of the given type and shape."""
+    if t.dtype != dtype:
+        raise GdnError(3, "%s is %s, not %s" % (name, t.dtype, dtype))
+    if tuple(t.shape) != shape:
+        raise GdnError(2, "%s has shape %s, not %s" % (name, tuple(t.shape), shape))
+    if t.device != device:
+        raise GdnError(1, "%s is on %s (all tensors must be on one CUDA device)" % (name, t.device))
+    if not t.is_contiguous():
+        raise GdnError(2, "%s must be contiguous" % name)
+
+
+def _call_ws(nbytes: int, device, workspace):
+    """The caller's workspace, or the cached one of this device and stream; while a graph is being
+    captured a fresh one, so that the graph keeps memory of its own."""
+    if workspace is not None:
+        if workspace.device != device or not workspace.is_contiguous():
+            raise GdnError(6, "workspace must be a contiguous tensor on the inputs' device")
+        return workspace
+    if torch.cuda.is_current_stream_capturing():
+        return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
+    return _workspace(nbytes, device)
+
+
+def qk_norm_rope(q, k, wq, wk, positions, v=None, rot: Optional[int] = None, base: float = 10000.0, eps: float = 1e-6,
+                 q_out=None, k_out=None, k_cache=None, v_cache=None, slots=None, want_k: bool = True, workspace=None,
+                 check: bool = False):
+    """Norms of queries and keys per head with the position rotation in the same pass (see
+    include/gdn.h). q [T,Hq,d], k, v [T,Hkv,d] (fp32 or bf16; may be slices of a fused projection's
+    output); wq, wk [d] fp32 or None; positions [T] int32; rot rotated elements (None: all d, 0: none).
+    With slots [T] int32 the rotated keys and the values also go to k_cache, v_cache
+    [pages,Hkv,page_size,d]. Returns (q_out, k_out); k_out is None with want_k=False, for callers that
+    read the keys from the cache."""
+    lib = load_library()
+    dev, dtype = q.device, q.dtype
+    if dtype not in _DTYPE:
+        raise GdnError(3, "q is %s (float32 or bfloat16)" % dtype)
+    q_stride = _heads("q", q, dev, dtype)
+    T, Hq, d = q.shape
+    k_stride = _heads("k", k, dev, dtype, d=d)
+    Hkv = k.shape[1]
+    if k.shape[0] != T:
+        raise GdnError(2, "k has %d tokens, q %d" % (k.shape[0], T))
+    v_stride = 0
+    pages, page_size = 0, 0
+    if slots is not None:
+        if v is None or k_cache is None or v_cache is None:
+            raise GdnError(1, "slots needs v, k_cache and v_cache")
+        v_stride = _heads("v", v, dev, dtype, Hkv, d)
+        if v.shape[0] != T:
+            raise GdnError(2, "v has %d tokens, q %d" % (v.shape[0], T))
+        if k_cache.dim() != 4:
+            raise GdnError(2, "k_cache has shape %s" % (tuple(k_cache.shape),))
+        pages, page_size = k_cache.shape[0], k_cache.shape[2]
+        _flat("k_cache", k_cache, dev, dtype, (pages, Hkv, page_size, d))
+        _flat("v_cache", v_cache, dev, dtype, (pages, Hkv, page_size, d))
+        _flat("slots", slots, dev, torch.int32, (T,))
+    rot = d if rot is None else rot
+    for name, w in (("wq", wq), ("wk", wk)):
+        if w is not None:
+            _flat(name, w, dev, torch.float32, (d,))
+    if positions is not None:
+        _flat("positions", positions, dev, torch.int32, (T,))
+    with _on(dev):
+        if q_out is None:
+            q_out = torch.empty((T, Hq, d), dtype=dtype, device=dev)
+        else:
+            _flat("q_out", q_out, dev, dtype, (T, Hq, d))
+        if k_out is not None:
+            _flat("k_out", k_out, dev, dtype, (T, Hkv, d))
+        elif want_k:
+            k_out = torch.empty((T, Hkv, d), dtype=dtype, device=dev)
+        ws = _call_ws(256, dev, workspace)
+        _check(lib.gdn_qk_norm_rope(_at(q), q_stride, _at(k), k_stride, _at(v) if slots is not None else None, v_stride,
+                                    _at(wq), _at(wk), eps, _at(positions), T, Hq, Hkv, d, rot, base, _DTYPE[dtype],
+                                    _at(q_out), _at(k_out), _at(k_cache), _at(v_cache), _at(slots), pages, page_size,
+                                    ws.data_ptr(), ws.numel() * ws.element_size(), _stream_of(dev)))
+        if check:
+            _check(lib.gdn_chunk_fwd_check(_ptr(ws), ws.numel(), _stream()))
+    return q_out, k_out
+
+
+def attn_prefill(q, k, v, cu_seqlens=None, N: Optional[int] = None, max_len: Optional[int] = None, scale: float = 0.0,
+                 o=None, workspace=None, check: bool = False):
+    """Causal attention over whole prompts with grouped heads (see include/gdn.h): q [T,Hq,d], k, v
+    [T,Hkv,d] bf16 (d 64 or 128; may be slices of wider rows); cu_seqlens [N+1] int32 (device) or None
+    (N equal sequences, N from ``N``, else 1); max_len bounds the lengths (required with cu_seqlens);
+    scale <= 0 means 1 / sqrt(d). Returns o [T,Hq,d]."""
+    lib = load_library()
+    dev = q.device
+    q_stride = _heads("q", q, dev, torch.bfloat16)
+    T, Hq, d = q.shape
+    k_stride = _heads("k", k, dev, torch.bfloat16, d=d)
+    Hkv = k.shape[1]
+    v_stride = _heads("v", v, dev, torch.bfloat16, Hkv, d)
+    if k.shape[0] != T or v.shape[0] != T:
+        raise GdnError(2, "q, k and v have %d, %d and %d tokens" % (T, k.shape[0], v.shape[0]))
+    if cu_seqlens is not None:
+        N = cu_seqlens.numel() - 1
+        _flat("cu_seqlens", cu_seqlens, dev, torch.int32, (N + 1,))
+        if max_len is None:
+            raise GdnError(2, "max_len is required with cu_seqlens")
+    else:
+        N = 1 if N is None else N
+        if N < 1:
+            raise GdnError(2, "N=%d must be >= 1" % N)
+        max_len = T // N
+    with _on(dev):
+        if o is None:
+            o = torch.empty((T, Hq, d), dtype=torch.bfloat16, device=dev)
+        else:
+            _flat("o", o, dev, torch.bfloat16, (T, Hq, d))
+        ws = _call_ws(256, dev, workspace)
+        _check(lib.gdn_attn_prefill(_at(q), q_stride, _at(k), k_stride, _at(v), v_stride, _at(cu_seqlens), N, T, Hq, Hkv,
+                                    d, min(max_len, T), scale, GDN_BF16, _at(o), ws.data_ptr(),
+                                    ws.numel() * ws.element_size(), _stream_of(dev)))
+        if check:
+            _check(lib.gdn_chunk_fwd_check(_ptr(ws), ws.numel(), _stream()))
     return o
 
 

@@ -1,0 +1,258 @@
+"""The attention layer's operators (gdn_qk_norm_rope, gdn_attn_prefill) against the fp64 oracle
+(oracle.attention_layer), element by element.
+
+Bounds, per element (u = 2^-8 the half step of bf16, e = 2^-24 that of fp32):
+* qk_norm_rope: with b the sum of the magnitudes of the element's terms, b (d / 2 + 32) e for the
+  fp32 arithmetic (d roundings in the mean, halved by the root; a few ulp each for the reciprocal
+  root, weight, angle, sine, cosine and the two products), and u |y| when y is bf16.
+* attention: the output's rounding u |o|; the weights' rounding u a with a = sum_j p_j |v_j|; the
+  scores' fp32 sums, 2 d e |scale| max|q| max|k| each (the tensor core may truncate: 2 e a step),
+  which moves a weight against the others by twice that; the sums over the n keys, 2 n e a.
+"""
+import numpy as np
+import pytest
+import torch
+
+from oracle import attention_layer as al
+from linear_attention_recurrent_chunked_b200 import gdn
+
+pytestmark = pytest.mark.gpu
+U, E = 2.0 ** -8, 2.0 ** -24
+BF, F32 = torch.bfloat16, torch.float32
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    gdn.load_library()
+
+
+def f64(t):
+    return t.detach().double().cpu().numpy()
+
+
+def randn(gen, *shape, dtype=BF):
+    return torch.randn(shape, generator=gen).to(dtype)
+
+
+def close(got, ref, tol):
+    got = f64(got)
+    assert np.isfinite(got).all()
+    bad = np.abs(got - ref) > tol
+    assert not bad.any(), ("%d of %d off, worst by %.3g times its bound" %
+                           (bad.sum(), bad.size, (np.abs(got - ref) / np.maximum(tol, 1e-300)).max()))
+
+
+def rope_tol(y, bound, d, dtype):
+    return bound * (d / 2 + 32) * E + (U * np.abs(y) if dtype == BF else 0) + 1e-30
+
+
+def attn_tol(o, a, q, k, d, n, scale=None):
+    scale = d ** -0.5 if scale is None else scale
+    big = scale * np.linalg.norm(f64(q), axis=-1).max() * np.linalg.norm(f64(k), axis=-1).max() if q.numel() else 0.0
+    return U * (np.abs(o) + a) * (1 + U) + a * (4 * d * E * big + 2 * n * E) + 1e-30
+
+
+# ------------------------------------------------------------------ qk_norm_rope
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("T,Hq,Hkv,d,rot", [(1, 1, 1, 64, 64), (3, 5, 1, 128, 32), (33, 16, 4, 128, 128), (2, 3, 3, 64, 16),
+                                            (7, 4, 2, 128, 0), (1500, 2, 1, 64, 32)])
+def test_norm_rope_matches(T, Hq, Hkv, d, rot, dtype):
+    gen = torch.Generator().manual_seed(T)
+    qkv = randn(gen, T, Hq + 2 * Hkv, d, dtype=dtype)
+    wq, wk = randn(gen, d, dtype=F32), randn(gen, d, dtype=F32)
+    pos = torch.randint(-5, 1 << 20, (T,), generator=gen, dtype=torch.int32)
+    pos[-1] = 2 ** 31 - 1
+    page = 16
+    pages = T // page + 2
+    slots = torch.randperm(pages * page, generator=gen)[:T].to(torch.int32)
+    slots[T // 2] = -1 if T > 2 else slots[T // 2]
+    dev = qkv.cuda()
+    kc = torch.full((pages, Hkv, page, d), 7.0, dtype=dtype, device="cuda")
+    vc = torch.full((pages, Hkv, page, d), 9.0, dtype=dtype, device="cuda")
+    q, k = gdn.qk_norm_rope(dev[:, :Hq], dev[:, Hq:Hq + Hkv], wq.cuda(), wk.cuda(), pos.cuda(), v=dev[:, Hq + Hkv:], rot=rot,
+                            k_cache=kc, v_cache=vc, slots=slots.cuda(), check=True)
+    qr, qb = al.norm_rope(qkv[:, :Hq], wq, pos, rot)
+    kr, kb = al.norm_rope(qkv[:, Hq:Hq + Hkv], wk, pos, rot)
+    close(q, qr, rope_tol(qr, qb, d, dtype))
+    close(k, kr, rope_tol(kr, kb, d, dtype))
+    # the cache: exactly the keys that came back and the values that went in; other slots untouched
+    want_k, want_v = torch.full_like(kc, 7.0), torch.full_like(vc, 9.0)
+    for t, s in enumerate(slots.tolist()):
+        if s >= 0:
+            want_k[s // page, :, s % page], want_v[s // page, :, s % page] = k[t], dev[t, Hq + Hkv:]
+    assert torch.equal(kc, want_k) and torch.equal(vc, want_v)
+    # without the cache, without k, in place: the same bits
+    q2, k2 = gdn.qk_norm_rope(dev[:, :Hq], dev[:, Hq:Hq + Hkv], wq.cuda(), wk.cuda(), pos.cuda(), rot=rot)
+    assert torch.equal(q2, q) and torch.equal(k2, k)
+    qi, ki = dev[:, :Hq].contiguous(), dev[:, Hq:Hq + Hkv].contiguous()
+    gdn.qk_norm_rope(qi, ki, wq.cuda(), wk.cuda(), pos.cuda(), rot=rot, q_out=qi, k_out=ki)
+    assert torch.equal(qi, q) and torch.equal(ki, k)
+    assert gdn.qk_norm_rope(dev[:, :Hq], dev[:, Hq:Hq + Hkv], wq.cuda(), wk.cuda(), pos.cuda(), v=dev[:, Hq + Hkv:], rot=rot,
+                            k_cache=kc, v_cache=vc, slots=slots.cuda(), want_k=False)[1] is None
+
+
+def test_norm_rope_options_and_extremes():
+    """No weights; base and eps; rows of zeros (eps decides), tiny and huge rows in fp32."""
+    gen = torch.Generator().manual_seed(9)
+    x = randn(gen, 6, 2, 64, dtype=F32)
+    x[1], x[2], x[3] = 0.0, x[2] * 1e-12, x[3] * 1e15
+    pos = torch.arange(6, dtype=torch.int32) * 1000
+    q, _ = gdn.qk_norm_rope(x.cuda(), x[:, :1].contiguous().cuda(), None, None, pos.cuda(), base=1e6, eps=1e-5, check=True)
+    y, b = al.norm_rope(x, None, pos, 64, base=1e6, eps=float(np.float32(1e-5)))
+    close(q, y, rope_tol(y, b, 64, F32))
+    assert (f64(q)[1] == 0).all()
+
+
+def test_norm_rope_bad_slots_are_reported_and_skipped():
+    gen = torch.Generator().manual_seed(3)
+    x = randn(gen, 5, 2, 64).cuda()
+    pos = torch.arange(5, dtype=torch.int32).cuda()
+    for bad in (32, -2, 2 ** 31 - 1, -2 ** 31):
+        kc, vc = torch.zeros((2, 2, 16, 64), dtype=BF, device="cuda"), torch.zeros((2, 2, 16, 64), dtype=BF, device="cuda")
+        slots = torch.tensor([0, 31, bad, -1, 5], dtype=torch.int32).cuda()
+        with pytest.raises(gdn.GdnError) as e:
+            gdn.qk_norm_rope(x, x, None, None, pos, v=x, k_cache=kc, v_cache=vc, slots=slots, check=True)
+        assert e.value.status == 10
+        assert torch.equal(vc[0, :, 0], x[0]) and torch.equal(vc[1, :, 15], x[1]) and torch.equal(vc[0, :, 5], x[4])
+        vc[0, :, 0] = vc[1, :, 15] = vc[0, :, 5] = 0
+        assert not vc.any()
+    # the next good call clears the report
+    gdn.qk_norm_rope(x, x, None, None, pos, check=True)
+
+
+def test_norm_rope_no_tokens():
+    x = torch.zeros((0, 4, 64), dtype=BF, device="cuda")
+    q, k = gdn.qk_norm_rope(x, x, None, None, torch.zeros(0, dtype=torch.int32, device="cuda"), check=True)
+    assert q.shape == (0, 4, 64) and k.shape == (0, 4, 64)
+
+
+# ------------------------------------------------------------------ attn_prefill
+
+def prompt(gen, lens, Hq, Hkv, d, std=1.0):
+    T = sum(lens)
+    q, k = randn(gen, T, Hq, d) * std, randn(gen, T, Hkv, d)
+    v = randn(gen, T, Hq + 2 * Hkv, d)
+    cu = torch.tensor(np.concatenate([[0], np.cumsum(lens)]), dtype=torch.int32)
+    return q.to(BF), k, v, cu
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("Hq,Hkv", [(1, 1), (2, 1), (6, 2), (8, 2), (5, 1), (7, 1), (16, 2), (16, 1), (3, 3), (13, 1)])
+def test_prefill_groups_and_ragged_lengths(Hq, Hkv, d):
+    lens = [1, 0, 130, 7, 257, 64]
+    gen = torch.Generator().manual_seed(Hq * 100 + d)
+    q, k, v, cu = prompt(gen, lens, Hq, Hkv, d)
+    v = v.cuda()[:, Hq + Hkv:]
+    o = gdn.attn_prefill(q.cuda(), k.cuda(), v, cu.cuda(), max_len=max(lens), check=True)
+    ref, a = al.prompt_attention(q, k, v, lens)
+    close(o, ref, attn_tol(ref, a, q, k, d, max(lens)))
+
+
+@pytest.mark.parametrize("lens", [[1], [2], [127], [128], [129], [255], [256], [513], [700, 1, 1, 1], [0, 0, 3]])
+def test_prefill_tile_edges(lens):
+    gen = torch.Generator().manual_seed(sum(lens))
+    q, k, v, cu = prompt(gen, lens, 4, 2, 128)
+    v = v[:, 6:].contiguous()
+    o = gdn.attn_prefill(q.cuda(), k.cuda(), v.cuda(), cu.cuda(), max_len=max(lens), check=True)
+    ref, a = al.prompt_attention(q, k, v, lens)
+    close(o, ref, attn_tol(ref, a, q, k, 128, max(lens)))
+
+
+@pytest.mark.parametrize("trend", ["rising", "falling", "spikes"])
+@pytest.mark.parametrize("d", [64, 128])
+def test_prefill_moving_maximum(trend, d):
+    """Scores up to about 30 that rise along the keys move the running maximum tile after tile, falling
+    ones never do, spikes do at single rows."""
+    T, Hq, Hkv = 600, 4, 1
+    gen = torch.Generator().manual_seed(5)
+    q, k, v, cu = prompt(gen, [T], Hq, Hkv, d)
+    u = torch.nn.functional.normalize(torch.randn(d, generator=gen), dim=0)
+    if trend == "spikes":
+        k[::97] = (12 * u).to(BF)
+        q[:] = (2.5 * d ** 0.5 * u).to(BF) * torch.rand((T, Hq, 1), generator=gen).to(BF)
+    else:
+        ramp = torch.linspace(0, 12, T) if trend == "rising" else torch.linspace(12, 0, T)
+        q[:] = (2.5 * d ** 0.5 * u).to(BF)
+        k = (ramp[:, None, None] * u + 0.1 * k.float()).to(BF)
+    v = v[:, Hq + Hkv:].contiguous()
+    o = gdn.attn_prefill(q.cuda(), k.cuda(), v.cuda(), check=True)
+    ref, a = al.prompt_attention(q, k, v, [T])
+    close(o, ref, attn_tol(ref, a, q, k, d, T))
+
+
+def test_prefill_equal_split_and_scale():
+    gen = torch.Generator().manual_seed(6)
+    q, k, v, _ = prompt(gen, [300, 300], 4, 4, 64)
+    v = v[:, 8:].contiguous()
+    o = gdn.attn_prefill(q.cuda(), k.cuda(), v.cuda(), N=2, scale=0.3, check=True)
+    ref, a = al.prompt_attention(q, k, v, [300, 300], scale=0.3)
+    close(o, ref, attn_tol(ref, a, q, k, 64, 300, 0.3))
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_prefill_neighbours_do_not_leak(d):
+    """NaN and infinity in a packed neighbour's rows leave a sequence's outputs as they were, bit for
+    bit; rows beyond the last sequence's end stay untouched."""
+    lens = [70, 90, 200]
+    gen = torch.Generator().manual_seed(7)
+    q, k, v, cu = prompt(gen, lens, 4, 2, d)
+    v = v[:, 6:].contiguous()
+    want = gdn.attn_prefill(q.cuda(), k.cuda(), v.cuda(), cu.cuda(), max_len=200, check=True)
+    for n in range(3):
+        q2, k2, v2 = q.clone(), k.clone(), v.clone()
+        a, b = int(cu[n]), int(cu[n + 1])
+        for x in (q2, k2, v2):
+            x[:a], x[b:] = float("nan"), float("inf")
+        got = gdn.attn_prefill(q2.cuda(), k2.cuda(), v2.cuda(), cu.cuda(), max_len=200, check=True)
+        assert torch.equal(got[a:b], want[a:b])
+
+
+def test_prefill_malformed_seqlens_reported_not_written():
+    gen = torch.Generator().manual_seed(8)
+    q, k, v, _ = prompt(gen, [256], 4, 2, 128)
+    v = v[:, 6:].contiguous()
+    for cu, most in (([0, 150, 100, 256], 150), ([0, 100, 200, 255], 128), ([1, 100, 200, 256], 128), ([0, 90, 220, 256], 128),
+                     ([0, -5, 200, 256], 256), ([0, 300, 200, 256], 256)):
+        o = torch.full_like(q, 7.0).cuda()
+        with pytest.raises(gdn.GdnError) as e:
+            gdn.attn_prefill(q.cuda(), k.cuda(), v.cuda(), torch.tensor(cu, dtype=torch.int32).cuda(), max_len=most, o=o, check=True)
+        assert e.value.status == 5
+        assert bool((o == 7.0).all())
+
+
+def test_prefill_long_rows_sampled():
+    """2500 tokens, 16 query heads on 4 key heads; all heads of sampled rows against the oracle."""
+    T, Hq, Hkv, d = 2500, 16, 4, 128
+    gen = torch.Generator().manual_seed(11)
+    q, k, v, _ = prompt(gen, [T], Hq, Hkv, d)
+    v = v[:, Hq + Hkv:].contiguous()
+    o = gdn.attn_prefill(q.cuda(), k.cuda(), v.cuda(), check=True)
+    assert torch.isfinite(o).all()
+    qf, kf, vf = f64(q), f64(k), f64(v)
+    for t in [0, 31, 32, 63, 64, 127, 128, 1024, 2303, 2304, 2498, 2499]:
+        for h in range(Hq):
+            ref, a = al._attend(qf[t, h][None], kf[:t + 1, h // 4], vf[:t + 1, h // 4], d ** -0.5, np.ones((1, t + 1), bool))
+            close(o[t, h][None], ref, attn_tol(ref, a, q[t], k, d, t + 1))
+
+
+def test_prefill_same_inputs_same_bits_and_graph_replay():
+    gen = torch.Generator().manual_seed(12)
+    lens = [300, 41]
+    q, k, v, cu = prompt(gen, lens, 4, 2, 128)
+    q, k, v, cu = q.cuda(), k.cuda(), v[:, 6:].contiguous().cuda(), cu.cuda()
+    want = gdn.attn_prefill(q, k, v, cu, max_len=300)
+    assert torch.equal(gdn.attn_prefill(q, k, v, cu, max_len=300), want)
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        s.wait_stream(torch.cuda.default_stream())
+        o = torch.zeros_like(q)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            gdn.attn_prefill(q, k, v, cu, max_len=300, o=o)
+        g.replay()
+        g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(o, want)
