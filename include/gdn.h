@@ -329,6 +329,32 @@ gdn_status gdn_attn_prefill(const void *q, int64_t q_stride, const void *k, int6
                             void *stream);
 
 /*
+ * Decode attention: one new token per sequence over the paged cache, with an optional prefix that all
+ * B sequences share and whose keys are then read once for the batch and not once per sequence:
+ *     o_b = sum_j softmax_j(scale * q_b . k_j) v_j
+ * with j over the prefix_len keys of the prefix and the lens[b] keys of sequence b (its new token's
+ * among them, where gdn_qk_norm_rope has put it). No key is masked otherwise.
+ *   q, o         [B][Hq][d] bf16, contiguous; o must not alias the inputs
+ *   page_table   [B][max_pages] int32: key t of sequence b is in page page_table[b][t / page_size] at
+ *                place t % page_size. Entries past the last key's page are not read; a page may stand
+ *                in several rows or several times. max_pages page_size <= 2^30.
+ *   lens         [B] int32, from 0 to max_pages page_size. With no key at all a sequence's o is zero.
+ *   prefix_pages [ceil(prefix_len / page_size)] int32 on the device, or NULL when prefix_len is 0. The
+ *                prefix may end inside a page; a sequence's own keys start on a page of their own.
+ *   scale > 0, or <= 0 for 1 / sqrt(d); d 64 or 128; Hq / Hkv from 1 to 16; dtype GDN_BF16.
+ *   workspace    gdn_attn_decode_workspace_size(...) bytes, 256-byte aligned; contents on entry ignored
+ * A length or page number outside its range is recorded as GDN_ERR_PAGES: lengths are taken to the
+ * nearest bound and such a page reads as zeros, so that no access leaves the cache, and the outputs
+ * concerned are meaningless. What stale slots hold (NaN included) does not matter. Equal calls give
+ * equal bits.
+ */
+size_t gdn_attn_decode_workspace_size(int B, int Hq, int Hkv, int d, int prefix_len);
+gdn_status gdn_attn_decode(const void *q, const void *k_cache, const void *v_cache, int num_pages, int page_size,
+                           const int32_t *page_table, int max_pages, const int32_t *lens, const int32_t *prefix_pages,
+                           int prefix_len, int B, int Hq, int Hkv, int d, float scale, gdn_dtype dtype, void *o,
+                           void *workspace, size_t ws_bytes, void *stream);
+
+/*
  * The sequential (token-by-token) scan on the GPU: the same result as
  * gdn_chunk_fwd, computed one token at a time with the decode step's row
  * update. It is the comparator for the chunked path's speed-up (page 1,

@@ -90,6 +90,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
 
     Item it;
     if (PREFIX) {
+        if (blockIdx.x == 0 && tid == 0) *a.err = 0u;
+        asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the own keys' kernel needs nothing of this one
         const int b = blockIdx.x, rb = b / (a.Hkv * a.splits), rem = b - rb * a.Hkv * a.splits;
         it.head = rem / a.splits;
         it.split = rem - it.head * a.splits;
@@ -393,7 +395,32 @@ cudaError_t launch_prompt(AttnPrefill a, cudaStream_t st, const char **stage) {
     return cudaGetLastError();
 }
 
+template <int D>
+cudaError_t launch_prefix(AttnPrefill a, cudaStream_t st, const char **stage) {
+    cudaError_t e;
+    a.P = TQ / a.G;
+    a.blocks = (a.T_tot + 2 * a.P - 1) / (2 * a.P);
+    CUtensorMap tm_q, tm_k, tm_v;
+    *stage = "TMA descriptor encoding";
+    const uint64_t page = 1u << a.page_log, n = (uint64_t)a.num_pages * a.Hkv;
+    if ((e = attn::make_map(&tm_q, a.q, D, a.Hq, a.T_tot, D, (uint64_t)a.Hq * D, a.G, a.P)) != cudaSuccess) return e;
+    if ((e = attn::make_map(&tm_k, a.k, D, page, n, D, page * D, (uint32_t)page, 1)) != cudaSuccess) return e;
+    if ((e = attn::make_map(&tm_v, a.v, D, page, n, D, page * D, (uint32_t)page, 1)) != cudaSuccess) return e;
+    *stage = "attn_prefix";
+    auto kern = k_attn_prefill<D, true>;
+    if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Layout<D>::SMEM)) != cudaSuccess)
+        return e;
+    void *pr = prof_start("attn_prefix", st);
+    kern<<<a.blocks * a.Hkv * a.splits, NTHREADS, Layout<D>::SMEM, st>>>(tm_q, tm_k, tm_v, a);
+    prof_stop(pr);
+    return cudaGetLastError();
+}
+
 }  // namespace
+
+cudaError_t launch_attn_prefix(const AttnPrefill &a, int d, cudaStream_t st, const char **stage) {
+    return d == 64 ? launch_prefix<64>(a, st, stage) : launch_prefix<128>(a, st, stage);
+}
 
 cudaError_t launch_attn_prefill(const AttnPrefill &a, int d, cudaStream_t st, const char **stage) {
     if (a.T_tot == 0 || a.max_len == 0) {

@@ -517,6 +517,87 @@ gdn_status gdn_attn_prefill(const void *q, int64_t q_stride, const void *k, int6
     return ok();
 }
 
+// Regions of gdn_attn_decode's workspace, each 256-byte aligned.
+struct DecodeWs {
+    size_t slot_o, slot_ml, part_o, part_ml, total;
+    DecodeWs(int B, int Hq, int Hkv, int d, int prefix_len) {
+        const size_t slots = gdn::attn_decode_slots(B, Hq, Hkv, prefix_len);
+        const size_t parts = (size_t)gdn::attn_decode_splits(B, Hq, Hkv, prefix_len) * B * Hq;
+        auto up = [](size_t n) { return (n + 255) / 256 * 256; };
+        slot_o = kErrWordBytes;
+        slot_ml = slot_o + up(slots * d * sizeof(float));
+        part_o = slot_ml + up(slots * sizeof(float2));
+        part_ml = part_o + up(parts * d * sizeof(float));
+        total = part_ml + up(parts * sizeof(float2));
+    }
+};
+static bool decode_sizes_ok(int B, int Hq, int Hkv, int d, int prefix_len) {
+    return B >= 1 && Hq >= 1 && Hkv >= 1 && Hq % Hkv == 0 && Hq / Hkv <= 16 && (d == 64 || d == 128) && prefix_len >= 0 &&
+           prefix_len <= 1 << 30 && (double)B * Hq < 2.0e9;
+}
+
+size_t gdn_attn_decode_workspace_size(int B, int Hq, int Hkv, int d, int prefix_len) {
+    return decode_sizes_ok(B, Hq, Hkv, d, prefix_len) ? DecodeWs(B, Hq, Hkv, d, prefix_len).total : kErrWordBytes;
+}
+
+gdn_status gdn_attn_decode(const void *q, const void *k_cache, const void *v_cache, int num_pages, int page_size,
+                           const int32_t *page_table, int max_pages, const int32_t *lens, const int32_t *prefix_pages,
+                           int prefix_len, int B, int Hq, int Hkv, int d, float scale, gdn_dtype dtype, void *o,
+                           void *workspace, size_t ws_bytes, void *stream) {
+    if (dtype != GDN_BF16) return fail(GDN_ERR_DTYPE, "attention takes bf16 inputs only");
+    if (!decode_sizes_ok(B, Hq, Hkv, d, prefix_len))
+        return fail(GDN_ERR_SHAPE, "B=%d Hq=%d Hkv=%d d=%d prefix_len=%d unsupported (d 64 or 128, Hq a multiple of Hkv, at "
+                    "most 16 times it, a prefix of at most 2^30 keys)", B, Hq, Hkv, d, prefix_len);
+    if (!page_size_ok(page_size) || num_pages < 1 || (int64_t)num_pages * page_size > INT32_MAX ||
+        ((int64_t)num_pages + 1) * Hkv > INT32_MAX)
+        return fail(GDN_ERR_SHAPE, "num_pages=%d page_size=%d unsupported (page_size 16, 32, 64 or 128; at most 2^31-1 "
+                    "slots)", num_pages, page_size);
+    if (max_pages < 1 || (int64_t)max_pages * page_size > 1 << 30)
+        return fail(GDN_ERR_SHAPE, "max_pages=%d out of range (at least 1, at most 2^30 keys a sequence)", max_pages);
+    if (!q || !k_cache || !v_cache || !page_table || !lens || !o || (prefix_len > 0 && !prefix_pages))
+        return fail(GDN_ERR_NULL, "q, k_cache, v_cache, page_table, lens, o and (with prefix_len) prefix_pages are required");
+    const void *ptrs[] = {q, k_cache, v_cache, o};
+    for (const void *p : ptrs)
+        if (misaligned(p)) return fail(GDN_ERR_ALIGN, "pointer %p is not 16-byte aligned", p);
+    if ((reinterpret_cast<uintptr_t>(page_table) | reinterpret_cast<uintptr_t>(lens) |
+         reinterpret_cast<uintptr_t>(prefix_pages)) & 3u)
+        return fail(GDN_ERR_ALIGN, "page_table, lens and prefix_pages must be 4-byte aligned");
+    const DecodeWs w(B, Hq, Hkv, d, prefix_len);
+    if (!workspace || ws_bytes < w.total)
+        return fail(GDN_ERR_WORKSPACE, "workspace of %zu bytes given, %zu needed", workspace ? ws_bytes : 0, w.total);
+    if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
+        return fail(GDN_ERR_ALIGN, "workspace must be 256-byte aligned");
+    if (!(scale > 0.f)) scale = 1.f / sqrtf((float)d);
+    char *ws = static_cast<char *>(workspace);
+    gdn::AttnDecode a{};
+    a.q = static_cast<const __nv_bfloat16 *>(q);
+    a.k_cache = static_cast<const __nv_bfloat16 *>(k_cache);
+    a.v_cache = static_cast<const __nv_bfloat16 *>(v_cache);
+    a.table = page_table;
+    a.lens = lens;
+    a.prefix_pages = prefix_pages;
+    a.B = B;
+    a.Hq = Hq;
+    a.Hkv = Hkv;
+    a.G = Hq / Hkv;
+    a.max_pages = max_pages;
+    a.num_pages = num_pages;
+    while ((1 << a.page_log) < page_size) ++a.page_log;
+    a.prefix_len = prefix_len;
+    a.splits = gdn::attn_decode_splits(B, Hq, Hkv, prefix_len);
+    a.scale_log2 = scale * 1.4426950408889634f;
+    a.o = static_cast<__nv_bfloat16 *>(o);
+    a.err = reinterpret_cast<uint32_t *>(ws);
+    a.slot_o = reinterpret_cast<float *>(ws + w.slot_o);
+    a.slot_ml = reinterpret_cast<float2 *>(ws + w.slot_ml);
+    a.part_o = reinterpret_cast<float *>(ws + w.part_o);
+    a.part_ml = reinterpret_cast<float2 *>(ws + w.part_ml);
+    const char *stage = "";
+    const cudaError_t e = gdn::launch_attn_decode(a, d, static_cast<cudaStream_t>(stream), &stage);
+    if (e != cudaSuccess) return cuda_fail(e, stage);
+    return ok();
+}
+
 gdn_status gdn_debug_inject(int kind, unsigned wait_us) {
     if (kind != GDN_INJECT_NONE && kind != GDN_INJECT_WITHHOLD_LINK)
         return fail(GDN_ERR_SHAPE, "unknown injection kind %d", kind);

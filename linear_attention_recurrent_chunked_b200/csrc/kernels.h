@@ -99,6 +99,29 @@ struct AttnPrefill {
 };
 cudaError_t launch_attn_prefill(const AttnPrefill &a, int d, cudaStream_t st, const char **stage);
 
+// The same kernel without the mask over a cached prefix that a batch shares: partial results per split.
+cudaError_t launch_attn_prefix(const AttnPrefill &a, int d, cudaStream_t st, const char **stage);
+
+// Attention of one token per sequence over the paged cache (see gdn_attn_decode).
+constexpr int kDecodeCtas = 148;  // runs that the own keys are cut into: one per SM
+struct AttnDecode {
+    const __nv_bfloat16 *q, *k_cache, *v_cache;
+    const int32_t *table, *lens;  // [B][max_pages], [B]
+    const int32_t *prefix_pages;
+    int B, Hq, Hkv, G, max_pages, num_pages, page_log, prefix_len, splits;
+    float scale_log2;
+    __nv_bfloat16 *o;
+    uint32_t *err;
+    // pieces, G rows each: two slots per CTA, then (with a prefix) one per (sequence, key head)
+    float *slot_o;
+    float2 *slot_ml;
+    float *part_o;  // the prefix kernel's, per split
+    float2 *part_ml;
+};
+int attn_decode_splits(int B, int Hq, int Hkv, int prefix_len);
+size_t attn_decode_slots(int B, int Hq, int Hkv, int prefix_len);  // rows of d floats
+cudaError_t launch_attn_decode(const AttnDecode &a, int d, cudaStream_t st, const char **stage);
+
 // Failure injection for tests (set by gdn_debug_inject; off by default): the pipelined path's
 // first segment of head 0 withholds its end-state flag, and waits for flags give up after
 // flag_wait_ns (0 = the normal bound) instead of hanging.

@@ -41,6 +41,8 @@ SIGNATURES = {
                               _VP, _VP, _VP, _VP, _I, _I, _VP, _SZ, _VP]),
     "gdn_attn_prefill": (_I, [_VP, _I64, _VP, _I64, _VP, _I64, _VP, _I, _I, _I, _I, _I, _I, _F32, _I, _VP, _VP, _SZ,
                               _VP]),
+    "gdn_attn_decode_workspace_size": (_SZ, [_I, _I, _I, _I, _I]),
+    "gdn_attn_decode": (_I, [_VP, _VP, _VP, _I, _I, _VP, _I, _VP, _VP, _I, _I, _I, _I, _I, _F32, _I, _VP, _VP, _SZ, _VP]),
     "gdn_proj_w8": (_I, [_VP, _VP, _VP, _I, _I, _I, _I, _I, _VP, _VP, _VP, _VP, _VP, _VP, _SZ, _VP]),
     "gdn_decode_step": (_I, [_VP, _VP, _VP, _VP, _VP, _VP, _I, _I, _I, _I, _I, _VP, _VP]),
     "gdn_seq_scan": (_I, [_VP, _VP, _VP, _VP, _VP, _VP, _VP, _I, _I, _I, _I, _I, _I, _VP, _VP, _VP]),
@@ -390,6 +392,44 @@ def attn_prefill(q, k, v, cu_seqlens=None, N: Optional[int] = None, max_len: Opt
         _check(lib.gdn_attn_prefill(_at(q), q_stride, _at(k), k_stride, _at(v), v_stride, _at(cu_seqlens), N, T, Hq, Hkv,
                                     d, min(max_len, T), scale, GDN_BF16, _at(o), ws.data_ptr(),
                                     ws.numel() * ws.element_size(), _stream_of(dev)))
+        if check:
+            _check(lib.gdn_chunk_fwd_check(_ptr(ws), ws.numel(), _stream()))
+    return o
+
+
+def attn_decode(q, k_cache, v_cache, page_table, lens, prefix_pages=None, prefix_len: int = 0, scale: float = 0.0, o=None,
+                workspace=None, check: bool = False):
+    """Attention of one new token per sequence over the paged cache (see include/gdn.h): q [B,Hq,d]
+    bf16, k_cache, v_cache [pages,Hkv,page_size,d] bf16, page_table [B,max_pages] int32, lens [B] int32;
+    prefix_pages [n] int32 and prefix_len: a prefix that all sequences share. Returns o [B,Hq,d]."""
+    lib = load_library()
+    dev = q.device
+    if q.dim() != 3 or k_cache.dim() != 4 or page_table.dim() != 2:
+        raise GdnError(2, "q, k_cache, page_table have shapes %s, %s, %s" % (tuple(q.shape), tuple(k_cache.shape),
+                                                                              tuple(page_table.shape)))
+    B, Hq, d = q.shape
+    pages, Hkv, page_size, _ = k_cache.shape
+    _flat("q", q, dev, torch.bfloat16, (B, Hq, d))
+    _flat("k_cache", k_cache, dev, torch.bfloat16, (pages, Hkv, page_size, d))
+    _flat("v_cache", v_cache, dev, torch.bfloat16, (pages, Hkv, page_size, d))
+    _flat("page_table", page_table, dev, torch.int32, (B, page_table.shape[1]))
+    _flat("lens", lens, dev, torch.int32, (B,))
+    if prefix_len:
+        if prefix_pages is None:
+            raise GdnError(1, "prefix_len needs prefix_pages")
+        _flat("prefix_pages", prefix_pages, dev, torch.int32, (prefix_pages.numel(),))
+        if prefix_len > prefix_pages.numel() * page_size:
+            raise GdnError(2, "prefix_len=%d exceeds the %d prefix pages" % (prefix_len, prefix_pages.numel()))
+    with _on(dev):
+        if o is None:
+            o = torch.empty((B, Hq, d), dtype=torch.bfloat16, device=dev)
+        else:
+            _flat("o", o, dev, torch.bfloat16, (B, Hq, d))
+        ws = _call_ws(lib.gdn_attn_decode_workspace_size(B, Hq, Hkv, d, prefix_len), dev, workspace)
+        _check(lib.gdn_attn_decode(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), pages, page_size,
+                                   page_table.data_ptr(), page_table.shape[1], lens.data_ptr(),
+                                   _at(prefix_pages) if prefix_len else None, prefix_len, B, Hq, Hkv, d, scale, GDN_BF16,
+                                   o.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size(), _stream_of(dev)))
         if check:
             _check(lib.gdn_chunk_fwd_check(_ptr(ws), ws.numel(), _stream()))
     return o

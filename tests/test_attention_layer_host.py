@@ -77,3 +77,45 @@ def test_binding_refuses(lib):
     with pytest.raises(gdn.GdnError) as e:
         gdn.attn_prefill(bf(4, 512), bf(4, 2, 64), bf(4, 2, 64))
     assert e.value.status == 2
+
+
+DECODE = dict(q=FAKE, kc=FAKE, vc=FAKE, pages=64, page=16, table=FAKE, max_pages=8, lens=FAKE, prefix_pages=FAKE, prefix_len=100,
+              B=4, Hq=16, Hkv=4, d=128, scale=0.0, dt=1, o=FAKE, ws=FAKE, ws_bytes=1 << 30, stream=None)
+
+
+@pytest.mark.parametrize("over,status", [
+    (dict(dt=0), 3), (dict(d=96), 2), (dict(B=0), 2), (dict(Hq=0), 2), (dict(Hkv=0), 2), (dict(Hkv=3), 2), (dict(Hkv=0x7fffffff), 2),
+    (dict(Hq=68), 2), (dict(prefix_len=-1), 2), (dict(prefix_len=(1 << 30) + 1), 2), (dict(B=1 << 29), 2),
+    (dict(page=8), 2), (dict(page=48), 2), (dict(page=256), 2), (dict(pages=0), 2), (dict(pages=1 << 27), 2),
+    (dict(max_pages=0), 2), (dict(max_pages=(1 << 26) + 1), 2), (dict(pages=1 << 26, Hkv=32, Hq=32), 2),
+    (dict(q=None), 1), (dict(kc=None), 1), (dict(vc=None), 1), (dict(table=None), 1), (dict(lens=None), 1), (dict(o=None), 1),
+    (dict(prefix_pages=None), 1), (dict(q=MIS), 4), (dict(kc=MIS), 4), (dict(o=MIS), 4), (dict(table=ODD), 4), (dict(lens=ODD), 4),
+    (dict(prefix_pages=ODD), 4), (dict(ws=None), 6), (dict(ws_bytes=256), 6), (dict(ws=VP((1 << 20) + 16)), 4),
+])
+def test_attn_decode_refuses(lib, over, status):
+    assert lib.gdn_attn_decode(*{**DECODE, **over}.values()) == status
+    assert lib.gdn_last_error()
+
+
+def test_attn_decode_workspace_size(lib):
+    """At least the error word; the prefix adds a piece per sequence and per split."""
+    size = lib.gdn_attn_decode_workspace_size
+    plain = size(64, 16, 4, 128, 0)
+    assert plain >= 256 + 2 * 148 * 4 * 130 * 4
+    assert size(64, 16, 4, 128, 8192) >= plain + 64 * 16 * 130 * 4 * 2
+    assert size(0, 16, 4, 128, 0) == 256  # refused by the call
+    # a byte less than it says is refused
+    assert lib.gdn_attn_decode(*{**DECODE, "ws_bytes": size(4, 16, 4, 128, 100) - 1}.values()) == 6
+
+
+def test_binding_refuses_decode(lib):
+    from linear_attention_recurrent_chunked_b200 import gdn
+    bf = lambda *s: torch.zeros(s, dtype=torch.bfloat16)  # noqa: E731
+    i32 = lambda *s: torch.zeros(s, dtype=torch.int32)  # noqa: E731
+    good = dict(q=bf(2, 4, 64), k_cache=bf(3, 2, 16, 64), v_cache=bf(3, 2, 16, 64), page_table=i32(2, 1), lens=i32(2))
+    for over, status in ((dict(), 1), (dict(q=bf(2, 4, 64).float()), 3), (dict(v_cache=bf(3, 2, 16, 32)), 2), (dict(lens=i32(3)), 2),
+                         (dict(page_table=i32(2, 1).long()), 3), (dict(prefix_len=5), 1),
+                         (dict(prefix_len=33, prefix_pages=i32(2)), 2), (dict(q=bf(2, 4, 128)[..., :64]), 2)):
+        with pytest.raises(gdn.GdnError) as e:
+            gdn.attn_decode(**{**good, **over})
+        assert e.value.status == status, over

@@ -1,4 +1,4 @@
-"""The attention layer's operators (gdn_qk_norm_rope, gdn_attn_prefill) against the fp64 oracle
+"""The attention layer's operators (gdn_qk_norm_rope, gdn_attn_prefill, gdn_attn_decode) against the fp64 oracle
 (oracle.attention_layer), element by element.
 
 Bounds, per element (u = 2^-8 the half step of bf16, e = 2^-24 that of fp32):
@@ -256,3 +256,215 @@ def test_prefill_same_inputs_same_bits_and_graph_replay():
         g.replay()
     torch.cuda.synchronize()
     assert torch.equal(o, want)
+
+
+# ------------------------------------------------------------------ attn_decode
+
+def cached(gen, lens, Hq, Hkv, d, page, prefix=0, stale=float("nan")):
+    """A cache whose pages lie in a random order, stale slots and unused pages holding `stale`."""
+    counts = [-(-n // page) for n in lens]
+    shared = -(-prefix // page)
+    total = sum(counts) + shared + 2
+    order = torch.randperm(total, generator=gen).tolist()
+    kc, vc = (torch.full((total, Hkv, page, d), stale, dtype=BF) for _ in range(2))
+    table = torch.full((len(lens), max(1, max(counts))), -77, dtype=torch.int32)
+
+    def fill(pages, n):
+        for c in (kc, vc):
+            for i, p in enumerate(pages):
+                m = min(page, n - i * page)
+                c[p, :, :m] = randn(gen, Hkv, m, d)
+
+    for b, n in enumerate(lens):
+        mine = [order.pop() for _ in range(counts[b])]
+        table[b, :counts[b]] = torch.tensor(mine, dtype=torch.int32)
+        fill(mine, n)
+    pp = [order.pop() for _ in range(shared)]
+    fill(pp, prefix)
+    q = randn(gen, len(lens), Hq, d)
+    return dict(q=q, k_cache=kc, v_cache=vc, page_table=table, lens=torch.tensor(lens, dtype=torch.int32),
+                prefix_pages=torch.tensor(pp, dtype=torch.int32) if prefix else None, prefix_len=prefix)
+
+
+def on_gpu(w):
+    return {k: (x.cuda() if hasattr(x, "cuda") else x) for k, x in w.items()}
+
+
+def check_decode(w, scale=None, got=None):
+    if got is None:
+        got = gdn.attn_decode(**on_gpu(w), scale=scale or 0.0, check=True)
+    ref, a = al.decode_attention(w["q"], w["k_cache"], w["v_cache"], w["page_table"].tolist(), w["lens"].tolist(),
+                                 w["prefix_pages"], w["prefix_len"], scale)
+    d = w["q"].shape[2]
+    n = int(w["lens"].max()) + w["prefix_len"]
+    close(got, ref, attn_tol(ref, a, w["q"], torch.nan_to_num(w["k_cache"], 0.0, 0.0, 0.0), d, n, scale))
+    return got
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("Hq,Hkv,page", [(1, 1, 16), (2, 2, 32), (6, 2, 16), (16, 4, 64), (7, 1, 128), (8, 1, 16), (9, 1, 32),
+                                         (16, 1, 64), (32, 2, 16)])
+def test_decode_groups_pages_and_ragged_lengths(Hq, Hkv, page, d):
+    gen = torch.Generator().manual_seed(Hq * 10 + page)
+    check_decode(cached(gen, [1, 0, 15, 16, 17, 127, 128, 129, 400, 3], Hq, Hkv, d, page))
+
+
+@pytest.mark.parametrize("lens", [[0], [1], [16], [128], [129], [3000], [0, 0, 5], [1] * 300, [40000, 1]])
+def test_decode_lengths(lens):
+    gen = torch.Generator().manual_seed(sum(lens))
+    check_decode(cached(gen, lens, 4, 2, 128, 64))
+
+
+def test_decode_many_sequences_split_anywhere():
+    """More sequences than threads in the scan, with runs that end inside, at and across borders."""
+    gen = torch.Generator().manual_seed(21)
+    lens = torch.randint(0, 700, (333,), generator=gen).tolist()
+    check_decode(cached(gen, lens, 2, 1, 64, 32))
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("Hq,Hkv,page,prefix", [(4, 4, 16, 1), (16, 4, 16, 1000), (16, 4, 64, 2048), (5, 1, 32, 129), (16, 1, 128, 700),
+                                                (6, 2, 16, 128), (2, 1, 128, 5000)])
+def test_decode_shared_prefix(Hq, Hkv, page, prefix, d):
+    gen = torch.Generator().manual_seed(prefix + d)
+    check_decode(cached(gen, [0, 1, 200, 17, 0, 129, 64, 3, 5], Hq, Hkv, d, page, prefix))
+
+
+def test_decode_shared_prefix_many_sequences():
+    """Several row tiles of the prefix product, the last one partly filled; and no own keys at all."""
+    gen = torch.Generator().manual_seed(22)
+    check_decode(cached(gen, torch.randint(0, 60, (150,), generator=gen).tolist(), 4, 2, 128, 16, 500))
+    check_decode(cached(gen, [0] * 70, 8, 2, 64, 16, 300))
+
+
+@pytest.mark.parametrize("prefix", [0, 300])
+def test_decode_moving_maximum_and_scale(prefix):
+    """Scores between -40 and 40: pieces whose maxima are far apart join exactly enough."""
+    gen = torch.Generator().manual_seed(23)
+    w = cached(gen, [2000, 500, 3], 8, 2, 64, 16, prefix)
+    u = torch.nn.functional.normalize(torch.randn(64, generator=gen), dim=0)
+    w["q"] = (4 * u + 0.1 * w["q"].float()).to(BF)
+    ramp = torch.randn(w["k_cache"].shape[0], 1, 1, 1, generator=gen) * 4
+    w["k_cache"] = (w["k_cache"].float() * 0.3 + ramp * u).to(BF)
+    check_decode(w, scale=0.7)
+
+
+def test_decode_prefix_equals_the_same_keys_copied():
+    """A shared prefix gives what the same keys give when they stand in every sequence's own table."""
+    gen = torch.Generator().manual_seed(24)
+    w = cached(gen, [10, 0, 33, 128], 8, 2, 128, 16, 64)  # the prefix ends on a page's end
+    got = check_decode(w)
+    w2 = dict(w, page_table=torch.cat([w["prefix_pages"].expand(4, 4), w["page_table"]], 1).contiguous(), lens=w["lens"] + 64,
+              prefix_pages=None, prefix_len=0)
+    # the two orders of summation differ by rounding only: each within its bound of the same oracle
+    check_decode(w2)
+    ref, _ = al.decode_attention(w["q"], w["k_cache"], w["v_cache"], w["page_table"].tolist(), w["lens"].tolist(), w["prefix_pages"], 64)
+    ref2, _ = al.decode_attention(w2["q"], w2["k_cache"], w2["v_cache"], w2["page_table"].tolist(), w2["lens"].tolist())
+    assert np.allclose(ref, ref2, atol=1e-12) and got.shape == w["q"].shape
+
+
+def test_decode_bad_pages_and_lengths_are_reported():
+    """No access leaves the cache and the other sequences' rows stay right."""
+    gen = torch.Generator().manual_seed(25)
+    for prefix in (0, 40):
+        w = cached(gen, [40, 100, 7], 4, 2, 64, 16, prefix)
+        for name, place, bad in (("page_table", (1, 3), 10 ** 6), ("page_table", (1, 0), -1), ("lens", (1,), -5), ("lens", (1,), 10 ** 6)):
+            w2 = dict(w, **{name: w[name].clone()})
+            w2[name][place] = bad
+            if name == "lens" and bad > 0:
+                w2["page_table"][1] = w2["page_table"][1].clamp(min=0)
+            o = torch.zeros_like(w["q"]).cuda()
+            with pytest.raises(gdn.GdnError) as e:
+                gdn.attn_decode(**on_gpu(w2), o=o, check=True)
+            assert e.value.status == 10
+            ok = dict(w, q=w["q"][::2], page_table=w["page_table"][::2], lens=w["lens"][::2])
+            check_decode(ok, got=o[::2])
+        if prefix:
+            w2 = dict(w, prefix_pages=torch.tensor([10 ** 6, -1, 0], dtype=torch.int32))
+            with pytest.raises(gdn.GdnError) as e:
+                gdn.attn_decode(**on_gpu(w2), check=True)
+            assert e.value.status == 10
+        check_decode(w)  # and the next good call reports nothing
+
+
+def test_decode_same_bits_other_stream_and_graphs():
+    """Equal calls give equal bits; two graphs captured one after the other keep workspaces of their own
+    and may be replayed in any order and on two streams at once."""
+    gen = torch.Generator().manual_seed(26)
+    ws = [on_gpu(cached(gen, [700, 30, 1500], 8, 2, 128, 16, 200)), on_gpu(cached(gen, [90, 2500], 8, 2, 128, 32))]
+    want = [gdn.attn_decode(**w) for w in ws]
+    assert torch.equal(gdn.attn_decode(**ws[0]), want[0])
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        assert torch.equal(gdn.attn_decode(**ws[1]), want[1])
+    graphs, outs = [], []
+    for w in ws:
+        o = torch.zeros_like(w["q"])
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            gdn.attn_decode(**w, o=o)
+        graphs.append(g)
+        outs.append(o)
+    torch.cuda.synchronize()
+    for _ in range(3):
+        with torch.cuda.stream(s):
+            graphs[0].replay()
+        graphs[1].replay()
+    torch.cuda.synchronize()
+    for o, x in zip(outs, want):
+        assert torch.equal(o, x)
+
+
+# ------------------------------------------------------------------ the layer
+
+@pytest.mark.parametrize("d,rot", [(128, 32), (64, 64)])
+def test_layer_prompt_then_steps(d, rot):
+    """A layer in use: three prompts are normed, rotated, cached and attended; then each sequence
+    decodes four tokens from the cache. Each operator's result is held to the oracle of its formula on the
+    inputs it was given, and the cached keys of all steps to a second path: one long prompt."""
+    Hq, Hkv, page, steps = 8, 2, 16, 4
+    lens = [37, 130, 64]
+    gen = torch.Generator().manual_seed(d)
+    T, N = sum(lens), len(lens)
+    wq, wk = (1 + 0.1 * randn(gen, d, dtype=F32) for _ in range(2))
+    qkv = randn(gen, T + steps * N, Hq + 2 * Hkv, d)
+    dev = qkv.cuda()
+    per = -(-(max(lens) + steps) // page)
+    table = torch.randperm(N * per, generator=gen).reshape(N, per).to(torch.int32)
+    kc, vc = (torch.full((N * per, Hkv, page, d), float("nan"), dtype=BF, device="cuda") for _ in range(2))
+    slot = lambda b, t: int(table[b, t // page]) * page + t % page  # noqa: E731
+    pos = torch.tensor([t for n in lens for t in range(n)], dtype=torch.int32)
+    slots = torch.tensor([slot(b, t) for b, n in enumerate(lens) for t in range(n)], dtype=torch.int32)
+    cu = torch.tensor(np.concatenate([[0], np.cumsum(lens)]), dtype=torch.int32)
+    args = dict(rot=rot, k_cache=kc, v_cache=vc)
+    x = dev[:T]
+    q, k = gdn.qk_norm_rope(x[:, :Hq], x[:, Hq:Hq + Hkv], wq.cuda(), wk.cuda(), pos.cuda(), v=x[:, Hq + Hkv:], slots=slots.cuda(), check=True, **args)
+    o = gdn.attn_prefill(q, k, x[:, Hq + Hkv:], cu.cuda(), max_len=max(lens), check=True)
+    ref, a = al.prompt_attention(q, k, x[:, Hq + Hkv:], lens)
+    close(o, ref, attn_tol(ref, a, q, k, d, max(lens)))
+    have = list(lens)
+    seen = [[(qkv[int(cu[b]) + t], t) for t in range(n)] for b, n in enumerate(lens)]
+    for i in range(steps):
+        x = dev[T + i * N:T + (i + 1) * N]
+        pos = torch.tensor(have, dtype=torch.int32)
+        slots = torch.tensor([slot(b, have[b]) for b in range(N)], dtype=torch.int32)
+        q, _ = gdn.qk_norm_rope(x[:, :Hq], x[:, Hq:Hq + Hkv], wq.cuda(), wk.cuda(), pos.cuda(), v=x[:, Hq + Hkv:], slots=slots.cuda(),
+                                want_k=False, check=True, **args)
+        for b in range(N):
+            seen[b].append((qkv[T + i * N + b], have[b]))
+        have = [n + 1 for n in have]
+        o = gdn.attn_decode(q, kc, vc, table.cuda(), torch.tensor(have, dtype=torch.int32).cuda(), check=True)
+        ref, a = al.decode_attention(q, kc, vc, table.tolist(), have)
+        close(o, ref, attn_tol(ref, a, q, torch.nan_to_num(kc, 0.0), d, max(have)))
+    # the last step's rows are the last rows of prompts of everything seen so far
+    rows = torch.stack([x for s in seen for x, _ in s]).cuda()
+    pos = torch.tensor([t for s in seen for _, t in s], dtype=torch.int32).cuda()
+    q, k = gdn.qk_norm_rope(rows[:, :Hq], rows[:, Hq:Hq + Hkv], wq.cuda(), wk.cuda(), pos, rot=rot)
+    ends = np.cumsum(have)
+    cu = torch.tensor(np.concatenate([[0], ends]), dtype=torch.int32).cuda()
+    full = gdn.attn_prefill(q, k, rows[:, Hq + Hkv:], cu, max_len=max(have), check=True)
+    ref, a = al.prompt_attention(q, k, rows[:, Hq + Hkv:], have)
+    tol = attn_tol(ref, a, q, k, d, max(have))
+    close(full[ends - 1], ref[ends - 1], tol[ends - 1])
+    close(o, ref[ends - 1], tol[ends - 1])
