@@ -14,13 +14,20 @@
 // more than 8, so P <= 2^8 and O and the row sum l are seldom rescaled; o = O / l. P is rounded to
 // bf16 for the tensor core (at most 2^-8 of each weight); l sums the unrounded weights in fp32.
 //
-// One CTA holds two tiles (256 rows): while the softmax warps of one turn its S into P, the tensor
-// core works on the other. Roles:
+// One CTA holds two tiles (256 rows), and S comes in steps of 64 keys with two buffers per tile: the
+// softmax of one step of a tile runs while the tensor core computes the tile's next S and the other
+// tile's products. Roles:
 //   softmax  (2 x 4 warps)  one query row per thread
-//   loader   (1 warp)       TMA: Q once, then K and V tiles through one ring
-//   MMA      (1 warp)       per key tile and query tile: O += P V, then the next S once that product
-//                           has read P (a later tcgen05.mma is not ordered after an earlier one's
-//                           tensor-memory operand reads)
+//   loader   (1 warp)       TMA: Q once, then K and V tiles of 128 keys through one ring
+//   MMA      (1 warp)       per step and query tile: O += P V; then, one product later, the S two steps on
+//                           into the buffer that P was in, once that product has read P (a later
+//                           tcgen05.mma is not ordered after an earlier one's tensor-memory operand reads)
+// Bound: the tensor pipe. A step of a tile costs 8 products M=128 N=64 K=16 for S, whose operands both
+// come from shared memory (6 KB each at 128 bytes a cycle: 48 cycles, against 32 of arithmetic), and
+// 4 products M=128 N=128 K=16 for O (64 cycles each, V alone from shared memory): 640 cycles. With steps
+// of 128 keys S would run at its arithmetic rate (1024 cycles for twice the keys), but tensor memory then
+// holds one S buffer per tile beside O, and the chain S -> maximum -> weights -> O -> next S (4,250
+// cycles measured, half of it barrier and tensor-memory latencies) sets the pace instead.
 // Key tiles are counted from the sequence's start (or the prefix split's), so a tile may reach past
 // the end into another sequence's rows or stale cache slots; their weights are zero, and their V rows
 // are overwritten with zeros in shared memory before the product, so that a NaN there stays there.
@@ -28,6 +35,7 @@
 #include <math.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "attn_common.cuh"
 #include "chunk_common.cuh"
@@ -41,9 +49,10 @@ using attn::wait_bar;
 using attn::wait_bar_w;
 using bf16 = __nv_bfloat16;
 
-constexpr int TQ = 128, TK = 128;
+constexpr int TQ = 128, TK = 128;   // query rows of a tile, keys of a K or V tile in the ring
+constexpr int STEP = 64;            // keys of a step: half a ring tile
 constexpr float kRescale = 8.f;  // log2 units
-constexpr int NTHREADS = 320;
+constexpr int NTHREADS = 352;
 constexpr int W_LOAD = 8, W_MMA = 9;
 
 template <int D>
@@ -51,18 +60,20 @@ struct Layout {
     static constexpr uint32_t TILE = 128 * D * 2;      // D / 64 column blocks of 128 rows x 128 bytes
     static constexpr int NST = D == 128 ? 5 : 8;       // K and V tiles in the ring
     static constexpr uint32_t OFF_Q = 0, OFF_KV = 2 * TILE, OFF_BAR = OFF_KV + NST * TILE;
-    // barriers: Q landed, ring full / empty, and per query tile: S complete, P written, O += P V done
-    static constexpr int QFULL = 0, FULL = 1, EMPTY = FULL + NST, SFULL = EMPTY + NST, PREADY = SFULL + 2,
-                         PVD = PREADY + 2, FIN = PVD + 2, NBAR = FIN + 1;
+    // barriers: Q landed, ring full / empty, and per query tile and S buffer (2 u + buffer): S complete,
+    // P written, O += P V done; all products done
+    static constexpr int QFULL = 0, FULL = 1, EMPTY = FULL + NST, SFULL = EMPTY + NST, PREADY = SFULL + 4,
+                         PVD = PREADY + 4, FIN = PVD + 4, NBAR = FIN + 1;
     static constexpr uint32_t OFF_CTL = OFF_BAR + 8 * NBAR;
     static constexpr uint32_t SMEM = OFF_CTL + 16 + 1024;
-    static constexpr uint32_t TM_S = 0, TM_O = 256;    // S (and P over it) of tile u at u * 128, O at 256 + u * D
+    static constexpr uint32_t TM_S = 0, TM_O = 256;    // S (and P over it) of tile u, buffer b at (2 u + b) * 64, O at 256 + u * D
+    static constexpr int POLY = D == 64 ? 2 : 0;       // of every 8 weights, those that the FMA pipe computes: see the softmax
 };
 
-// What a CTA works on: query positions [pos0, pos0 + 2 P) of `rows` rows from token `t0`, key tiles
-// [0, nk[u]) of each query tile, keys from k0 on, `keys` of them there.
+// What a CTA works on: query positions [pos0, pos0 + 2 P) of a sequence of `len` from token t0 on, ns0 and
+// ns1 steps of its two query tiles (ns1 is 0 or at least ns0) over the keys from k0 on, `keys` of them there.
 struct Item {
-    int t0, len, pos0, head, k0, keys, nk0, nk1, split;
+    int t0, len, pos0, head, k0, keys, ns0, ns1, split;
 };
 
 // cu_seqlens malformed: the same answer from every thread of the CTA.
@@ -74,6 +85,63 @@ __device__ __forceinline__ bool seqlens_bad(const AttnPrefill &a) {
     }
     if (threadIdx.x == 0) bad |= a.cu[0] != 0 || a.cu[a.N] != a.T_tot;
     return __syncthreads_or(bad);
+}
+
+// The products of query tile u, issued by one warp.
+template <int D, int U>
+__device__ __forceinline__ void mma_loop(std::integral_constant<int, U> u, int myns, int ns, uint32_t tm, uint32_t sb,
+                                         uint64_t *bar, Ctl *ctl, uint32_t *err) {
+    using L = Layout<D>;
+    const uint32_t id_s = tc::make_idesc_bf16(TQ, STEP, 0, 0);  // Q K^T: both K-major
+    const uint32_t id_o = tc::make_idesc_bf16(TQ, D, 0, 1);     // P V: V MN-major
+    const tc::Desc dq = tc::split_desc(tc::make_desc_sw128(sb + L::OFF_Q + u * L::TILE, 16, 1024));
+    const tc::Desc dk = tc::split_desc(tc::make_desc_sw128(sb + L::OFF_KV, 16, 1024));
+    const tc::Desc dv = tc::split_desc(tc::make_desc_sw128(sb + L::OFF_KV, 16384, 1024));
+    // the ring holds K of steps 2 t and 2 t + 1 as tile 2 t, V of them as tile 2 t + 1
+    auto full = [&](int c) { return wait_bar_w(&bar[L::FULL + c % L::NST], (uint32_t)((c / L::NST) & 1), ctl, err); };
+    auto issue_s = [&](int j) {
+        const int c = j & ~1;
+        const uint32_t kb = (uint32_t)(c % L::NST) * L::TILE + (j & 1) * (STEP * 128);
+        const uint32_t ts = tm + L::TM_S + (2 * u + (j & 1)) * 64;
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t off = (kk >> 2) * 16384 + (kk & 3) * 32;
+            tc::mma_bf16_off_w(ts, dq, off, dk, kb + off, id_s, kk > 0);
+        }
+        tc::mma_commit_w(&bar[L::SFULL + 2 * u + (j & 1)]);
+        if ((j & 1) || j + 1 == myns) tc::mma_commit_w(&bar[L::EMPTY + c % L::NST]);
+    };
+    bool ok = wait_bar_w(&bar[L::QFULL], 0, ctl, err) && full(0);
+    if (ok) {
+        tc::fence_after_sync();
+        if (myns > 0) issue_s(0);
+        if (myns > 1) issue_s(1);
+    }
+    for (int j = 0; ok && j < myns; ++j) {
+        const int b = j & 1, c = j | 1;
+        if (!(ok = full(c) && wait_bar_w(&bar[L::PREADY + 2 * u + b], (uint32_t)((j >> 1) & 1), ctl, err))) break;
+        tc::fence_after_sync();
+        const uint32_t vb = (uint32_t)(c % L::NST) * L::TILE + b * (STEP * 128);
+        const uint32_t ts = tm + L::TM_S + (2 * u + b) * 64;
+#pragma unroll
+        for (int kk = 0; kk < STEP / 16; ++kk)
+            tc::mma_bf16_ts_off_w(tm + L::TM_O + u * D, ts + 8 * kk, dv, vb + kk * 2048, id_o, (j > 0 || kk > 0) ? 1u : 0u);
+        tc::mma_commit_w(&bar[L::PVD + 2 * u + b]);
+        if (b || j + 1 == myns) tc::mma_commit_w(&bar[L::EMPTY + c % L::NST]);
+        if (j + 2 < myns) {
+            if (!(ok = full((j + 2) & ~1) && wait_bar_w(&bar[L::PVD + 2 * u + b], (uint32_t)((j >> 1) & 1), ctl, err))) break;
+            tc::fence_after_sync();
+            issue_s(j + 2);
+        }
+    }
+    // ring tiles that only the other query tile uses: freed as they come
+    for (int c = 2 * ((myns + 1) / 2); ok && c < 2 * ((ns + 1) / 2); ++c) {
+        ok = full(c);
+        if (ok && (threadIdx.x & 31) == 0) tc::mbar_arrive(&bar[L::EMPTY + c % L::NST]);
+    }
+    tc::mma_commit_w(&bar[L::FIN]);
+    if ((threadIdx.x & 31) == 0) attn::drain_bar(&bar[L::FIN], 0);
+    __syncwarp();
 }
 
 template <int D, bool PREFIX>
@@ -103,8 +171,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         const int k0 = (int)((int64_t)tiles * it.split / a.splits), k1 = (int)((int64_t)tiles * (it.split + 1) / a.splits);
         it.k0 = k0 * TK;
         it.keys = a.prefix_len - it.k0;
-        it.nk0 = k1 - k0;
-        it.nk1 = it.pos0 + P < it.len ? it.nk0 : 0;
+        it.ns0 = (min(it.keys, (k1 - k0) * TK) + STEP - 1) / STEP;
+        it.ns1 = it.pos0 + P < it.len ? it.ns0 : 0;
     } else {
         // blocks are numbered so that the query tiles with the most key tiles come first
         const int per = a.Hkv * a.N, r = blockIdx.x / per, rem = blockIdx.x - r * per;
@@ -126,16 +194,16 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         it.k0 = it.t0;
         it.keys = it.len;
         const int e0 = min(it.pos0 + P, it.len), e1 = min(it.pos0 + 2 * P, it.len);
-        it.nk0 = (e0 + TK - 1) / TK;
-        it.nk1 = e1 > it.pos0 + P ? (e1 + TK - 1) / TK : 0;
+        it.ns0 = (e0 + STEP - 1) / STEP;
+        it.ns1 = e1 > it.pos0 + P ? (e1 + STEP - 1) / STEP : 0;
     }
-    const int nk = max(it.nk0, it.nk1);
+    const int ns = max(it.ns0, it.ns1), nk = (ns + 1) / 2;  // steps, ring tiles
 
     uint64_t *bar = reinterpret_cast<uint64_t *>(smem + L::OFF_BAR);
     Ctl *ctl = reinterpret_cast<Ctl *>(smem + L::OFF_CTL);
     if (warp == W_MMA) tc::tmem_alloc(&ctl->tmem, 512);
     if (tid == W_LOAD * 32) {
-        for (int i = 0; i < L::NBAR; ++i) tc::mbar_init(&bar[i], (i == L::PREADY || i == L::PREADY + 1) ? 128u : 1u);
+        for (int i = 0; i < L::NBAR; ++i) tc::mbar_init(&bar[i], (i >= L::PREADY && i < L::PREADY + 4) ? 128u : (i == L::FIN || (i >= L::EMPTY && i < L::SFULL)) ? 2u : 1u);
         ctl->abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -147,8 +215,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     if (warp == W_LOAD) {
         if (lane == 0) {
             const uint32_t bytes = (uint32_t)(a.G * P) * 128u * (D / 64);
-            tc::mbar_arrive_expect_tx(&bar[L::QFULL], it.nk1 ? 2 * bytes : bytes);
-            for (int u = 0; u < (it.nk1 ? 2 : 1); ++u)
+            tc::mbar_arrive_expect_tx(&bar[L::QFULL], it.ns1 ? 2 * bytes : bytes);
+            for (int u = 0; u < (it.ns1 ? 2 : 1); ++u)
 #pragma unroll
                 for (int hf = 0; hf < D / 64; ++hf)
                     tc::tma_load_3d(sb + L::OFF_Q + u * L::TILE + hf * 16384, &tm_q, &bar[L::QFULL], 64 * hf, it.head * a.G,
@@ -196,89 +264,46 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         }
         __syncwarp();
     } else if (warp == W_MMA) {
-        const uint32_t id_s = tc::make_idesc_bf16(TQ, TK, 0, 0);  // Q K^T: both K-major
-        const uint32_t id_o = tc::make_idesc_bf16(TQ, D, 0, 1);   // P V: V MN-major
-        const tc::Desc dq = tc::split_desc(tc::make_desc_sw128(sb + L::OFF_Q, 16, 1024));
-        const tc::Desc dk = tc::split_desc(tc::make_desc_sw128(sb + L::OFF_KV, 16, 1024));
-        const tc::Desc dv = tc::split_desc(tc::make_desc_sw128(sb + L::OFF_KV, 16384, 1024));
-        // the ring holds K_j as tile 2 j and V_j as tile 2 j + 1
-        auto full = [&](int c) { return wait_bar_w(&bar[L::FULL + c % L::NST], (uint32_t)((c / L::NST) & 1), ctl, a.err); };
-        auto issue_s = [&](int u, int j) {
-            const uint32_t kb = (uint32_t)((2 * j) % L::NST) * L::TILE;
-#pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) {
-                const uint32_t off = (kk >> 2) * 16384 + (kk & 3) * 32;
-                tc::mma_bf16_off_w(tm + L::TM_S + u * 128, dq, u * L::TILE + off, dk, kb + off, id_s, kk > 0);
-            }
-            tc::mma_commit_w(&bar[L::SFULL + u]);
-        };
-        const int nku[2] = {it.nk0, it.nk1};
-        bool ok = wait_bar_w(&bar[L::QFULL], 0, ctl, a.err) && full(0);
-        if (ok) {
-            tc::fence_after_sync();
-            issue_s(0, 0);
-            if (it.nk1) issue_s(1, 0);
-            tc::mma_commit_w(&bar[L::EMPTY]);
-        }
-        for (int j = 0; ok && j < nk; ++j) {
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                if (!ok || j >= nku[u]) continue;
-                if (!(ok = wait_bar_w(&bar[L::PREADY + u], (uint32_t)(j & 1), ctl, a.err) && full(2 * j + 1))) continue;
-                tc::fence_after_sync();
-                const uint32_t vb = (uint32_t)((2 * j + 1) % L::NST) * L::TILE;
-#pragma unroll
-                for (int kk = 0; kk < TK / 16; ++kk)
-                    tc::mma_bf16_ts_off_w(tm + L::TM_O + u * D, tm + L::TM_S + u * 128 + 8 * kk, dv, vb + kk * 2048, id_o,
-                                          (j > 0 || kk > 0) ? 1u : 0u);
-                tc::mma_commit_w(&bar[L::PVD + u]);
-                if (u == 1 || j >= nku[1]) tc::mma_commit_w(&bar[L::EMPTY + (2 * j + 1) % L::NST]);
-                if (j + 1 < nku[u]) {
-                    if (!(ok = full(2 * j + 2) && wait_bar_w(&bar[L::PVD + u], (uint32_t)(j & 1), ctl, a.err))) continue;
-                    tc::fence_after_sync();
-                    issue_s(u, j + 1);
-                    if (u == 1 || j + 1 >= nku[1]) tc::mma_commit_w(&bar[L::EMPTY + (2 * j + 2) % L::NST]);
-                }
-            }
-        }
-        tc::mma_commit_w(&bar[L::FIN]);
-        if (lane == 0) attn::drain_bar(&bar[L::FIN], 0);
-        __syncwarp();
+        mma_loop<D>(std::integral_constant<int, 0>(), it.ns0, ns, tm, sb, bar, ctl, a.err);
+    } else if (warp == W_MMA + 1) {
+        mma_loop<D>(std::integral_constant<int, 1>(), it.ns1, ns, tm, sb, bar, ctl, a.err);
     } else {
         // ---------------------------------------------------------------- softmax (one query row per thread)
         const int u = warp >> 2, r = tid & 127;
         const uint32_t tl = tm + ((uint32_t)((warp & 3) * 32) << 16);
-        const uint32_t ts = tl + L::TM_S + u * 128, to = tl + L::TM_O + u * D;
-        const int mynk = u ? it.nk1 : it.nk0;
+        const uint32_t to = tl + L::TM_O + u * D;
+        const int myns = u ? it.ns1 : it.ns0;
         const int pos = it.pos0 + u * P + r / a.G;  // position within the sequence
         const int first = it.pos0 + u * P;          // the tile's first position
         const float sc = a.scale_log2;
         float m_ref = -INFINITY, l = 0.f;
         bool ok = true;
-        for (int j = 0; ok && j < mynk; ++j) {
-            if (!(ok = wait_bar_w(&bar[L::SFULL + u], (uint32_t)(j & 1), ctl, a.err))) break;
+        for (int j = 0; ok && j < myns; ++j) {
+            const int sbuf = 2 * u + (j & 1);
+            const uint32_t ts = tl + L::TM_S + sbuf * 64;
+            if (!(ok = wait_bar_w(&bar[L::SFULL + sbuf], (uint32_t)((j >> 1) & 1), ctl, a.err))) break;
             tc::fence_after_sync();
-            float s[128];
-#pragma unroll
-            for (int c0 = 0; c0 < 128; c0 += 32) {
-                float x[32];
-                tc::tmem_ld32(ts + c0, x);
-#pragma unroll
-                for (int i = 0; i < 32; ++i) s[c0 + i] = x[i];
-            }
             // keys beyond this row's position, or beyond the prefix, are masked
-            const int lim = (PREFIX ? it.keys - 1 : pos) - j * TK;
-            if (PREFIX ? lim < TK - 1 : first - j * TK < TK - 1) {
+            uint32_t s[2][32];
+            attn::tmem_ld32x(ts, s[0]);
+            attn::tmem_ld32x(ts + 32, s[1]);
+            tc::tmem_wait_ld(s[0]);
+            tc::tmem_wait_ld(s[1]);
+            if (PREFIX ? it.keys - j * STEP < STEP : first - j * STEP < STEP - 1) {
+                const int lim = (PREFIX ? it.keys - 1 : pos) - j * STEP;
 #pragma unroll
-                for (int i = 0; i < 128; ++i) s[i] = (i <= lim) ? s[i] : -INFINITY;
+                for (int i = 0; i < STEP; ++i)
+                    if (i > lim) s[i >> 5][i & 31] = 0xFF800000u;  // -inf
             }
-            float pm[8];
+            auto S = [&](int i) { return __uint_as_float(s[i >> 5][i & 31]); };
+            float pm[4];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) pm[i] = -INFINITY;
+            for (int i = 0; i < 4; ++i) pm[i] = fmaxf(S(2 * i), S(2 * i + 1));
 #pragma unroll
-            for (int i = 0; i < 128; ++i) pm[i & 7] = fmaxf(pm[i & 7], s[i]);
-            const float mt = fmaxf(fmaxf(fmaxf(pm[0], pm[1]), fmaxf(pm[2], pm[3])),
-                                   fmaxf(fmaxf(pm[4], pm[5]), fmaxf(pm[6], pm[7]))) * sc;
+            for (int i = 8; i < STEP; i += 2) pm[(i >> 1) & 3] = attn::max3(pm[(i >> 1) & 3], S(i), S(i + 1));
+            const float mt = attn::max3(fmaxf(pm[0], pm[1]), pm[2], pm[3]) * sc;
+            // lazy rescale: a new reference maximum only when this step's exceeds it by more than kRescale. (A step
+            // may be masked whole for a row, mt = -inf, but never the first one.)
             float alpha = 1.f;
             const bool grow = mt > m_ref + kRescale;
             if (grow) {
@@ -287,53 +312,63 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                 l *= alpha;
             }
             if (j > 0 && __any_sync(0xffffffffu, grow)) {
-                if (!(ok = wait_bar_w(&bar[L::PVD + u], (uint32_t)((j - 1) & 1), ctl, a.err))) break;
+                const int pb = (j - 1) & 1;
+                if (!(ok = wait_bar_w(&bar[L::PVD + 2 * u + pb], (uint32_t)(((j - 1) >> 1) & 1), ctl, a.err))) break;
                 tc::fence_after_sync();
 #pragma unroll 1
                 for (int c0 = 0; c0 < D; c0 += 32) {
                     uint32_t w[32];
-                    tc::tmem_ld32_nowait(to + c0, w);
+                    attn::tmem_ld32x(to + c0, w);
                     tc::tmem_wait_ld(w);
 #pragma unroll
                     for (int i = 0; i < 32; ++i) w[i] = __float_as_uint(__uint_as_float(w[i]) * alpha);
                     tc::tmem_st32(to + c0, w);
                 }
             }
-            float ps[8];
+            // the weights as bf16 pairs over the first 32 columns of the buffer. For D = 64, where the products take
+            // half the time, the MUFU (8 cycles a warp's exponential) would be the bound, and the FMA pipe takes a quarter
+            uint64_t ps[2] = {0, 0};
+            const uint64_t sc2 = attn::pack2(sc, sc), mm2 = attn::pack2(-m_ref, -m_ref);
+            uint32_t w[32];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) ps[i] = 0.f;
-#pragma unroll
-            for (int c0 = 0; c0 < 128; c0 += 64) {
-                uint32_t w[32];
-#pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                    const float p0 = chunk::ex2(fmaf(s[c0 + 2 * i], sc, -m_ref));
-                    const float p1 = chunk::ex2(fmaf(s[c0 + 2 * i + 1], sc, -m_ref));
-                    ps[i & 7] += p0 + p1;
-                    w[i] = tc::pack_bf16x2(p0, p1);
+            for (int i = 0; i < 32; ++i) {
+                const uint64_t x = attn::fma2(attn::pack2(S(2 * i), S(2 * i + 1)), sc2, mm2);
+                float p0, p1;
+                if ((i & 3) >= 4 - L::POLY / 2) {
+                    attn::exp2_poly(x, p0, p1);
+                } else {
+                    attn::unpack2(x, p0, p1);
+                    p0 = chunk::ex2(p0);
+                    p1 = chunk::ex2(p1);
                 }
-                tc::tmem_st32(ts + c0 / 2, w);
+                ps[i & 1] = attn::add2(ps[i & 1], attn::pack2(p0, p1));
+                w[i] = tc::pack_bf16x2(p0, p1);
             }
-            l += ((ps[0] + ps[1]) + (ps[2] + ps[3])) + ((ps[4] + ps[5]) + (ps[6] + ps[7]));
-            if (it.keys - j * TK < TK) {
+            tc::tmem_st32(ts, w);
+            float a0, a1;
+            attn::unpack2(attn::add2(ps[0], ps[1]), a0, a1);
+            l += a0 + a1;
+            if (it.keys - j * STEP < STEP) {
                 // rows of V beyond the sequence or the prefix: another sequence's values or stale slots
-                const int c = 2 * j + 1, st = c % L::NST;
+                const int c = j | 1, st = c % L::NST, n = it.keys - j * STEP;
                 if (!(ok = wait_bar_w(&bar[L::FULL + st], (uint32_t)((c / L::NST) & 1), ctl, a.err))) break;
-                if (r >= it.keys - j * TK) {
+                if (r >= n && r < STEP) {
 #pragma unroll
                     for (int hf = 0; hf < D / 64; ++hf)
 #pragma unroll
                         for (int i = 0; i < 8; ++i)
-                            chunk::st_shared_v4(sb + L::OFF_KV + st * L::TILE + hf * 16384 + r * 128 + i * 16, 0, 0, 0, 0);
+                            chunk::st_shared_v4(sb + L::OFF_KV + st * L::TILE + hf * 16384 + ((j & 1) * STEP + r) * 128 + i * 16, 0, 0,
+                                                0, 0);
                 }
                 tc::fence_smem_to_async();
             }
             tc::tmem_st_wait();
             tc::fence_before_sync();
-            tc::mbar_arrive(&bar[L::PREADY + u]);
+            tc::mbar_arrive(&bar[L::PREADY + sbuf]);
         }
-        if (ok && mynk) ok = wait_bar_w(&bar[L::PVD + u], (uint32_t)((mynk - 1) & 1), ctl, a.err);
-        if (ok && mynk) {
+        if (ok && myns)
+            ok = wait_bar_w(&bar[L::PVD + 2 * u + ((myns - 1) & 1)], (uint32_t)(((myns - 1) >> 1) & 1), ctl, a.err);
+        if (ok && myns) {
             tc::fence_after_sync();
             const bool valid = r < a.G * P && pos < it.len;
             const int64_t row = (int64_t)(it.t0 + pos) * a.Hq + it.head * a.G + r % a.G;
