@@ -52,7 +52,7 @@ using bf16 = __nv_bfloat16;
 constexpr int TQ = 128, TK = 128;   // query rows of a tile, keys of a K or V tile in the ring
 constexpr int STEP = 64;            // keys of a step: half a ring tile
 constexpr float kRescale = 8.f;  // log2 units
-constexpr int NTHREADS = 352;
+constexpr int NTHREADS = 416;
 constexpr int W_LOAD = 8, W_MMA = 9;
 
 template <int D>
@@ -60,13 +60,14 @@ struct Layout {
     static constexpr uint32_t TILE = 128 * D * 2;      // D / 64 column blocks of 128 rows x 128 bytes
     static constexpr int NST = D == 128 ? 5 : 8;       // K and V tiles in the ring
     static constexpr uint32_t OFF_Q = 0, OFF_KV = 2 * TILE, OFF_BAR = OFF_KV + NST * TILE;
-    // barriers: Q landed, ring full / empty, and per query tile and S buffer (2 u + buffer): S complete,
-    // P written, O += P V done; all products done
-    static constexpr int QFULL = 0, FULL = 1, EMPTY = FULL + NST, SFULL = EMPTY + NST, PREADY = SFULL + 4,
-                         PVD = PREADY + 4, FIN = PVD + 4, NBAR = FIN + 1;
+    // barriers: Q landed, ring full / empty, per query tile: S complete, S read; per query tile and P buffer
+    // (2 u + buffer): P written, O += P V done; all products done
+    static constexpr int QFULL = 0, FULL = 1, EMPTY = FULL + NST, SFULL = EMPTY + NST, SFREE = SFULL + 2,
+                         PREADY = SFREE + 2, PVD = PREADY + 4, FIN = PVD + 4, NBAR = FIN + 1;
     static constexpr uint32_t OFF_CTL = OFF_BAR + 8 * NBAR;
     static constexpr uint32_t SMEM = OFF_CTL + 16 + 1024;
-    static constexpr uint32_t TM_S = 0, TM_O = 256;    // S (and P over it) of tile u, buffer b at (2 u + b) * 64, O at 256 + u * D
+    // tensor memory columns: S of tile u at u * 64, P of tile u, buffer b at 128 + (2 u + b) * 32, O at 256 + u * D
+    static constexpr uint32_t TM_S = 0, TM_P = 128, TM_O = 256;
     static constexpr int POLY = D == 64 ? 2 : 0;       // of every 8 weights, those that the FMA pipe computes: see the softmax
 };
 
@@ -87,61 +88,74 @@ __device__ __forceinline__ bool seqlens_bad(const AttnPrefill &a) {
     return __syncthreads_or(bad);
 }
 
-// The products of query tile u, issued by one warp.
-template <int D, int U>
-__device__ __forceinline__ void mma_loop(std::integral_constant<int, U> u, int myns, int ns, uint32_t tm, uint32_t sb,
-                                         uint64_t *bar, Ctl *ctl, uint32_t *err) {
+// The ring holds K of steps 2 t and 2 t + 1 as tile 2 t, V of them as tile 2 t + 1. A tile is freed by two
+// arrivals, one for each query tile: the commit of that query tile's last product on it, or a plain arrival
+// where it has none.
+template <int D>
+__device__ __forceinline__ bool ring_full(uint64_t *bar, int c, Ctl *ctl, uint32_t *err) {
     using L = Layout<D>;
-    const uint32_t id_s = tc::make_idesc_bf16(TQ, STEP, 0, 0);  // Q K^T: both K-major
-    const uint32_t id_o = tc::make_idesc_bf16(TQ, D, 0, 1);     // P V: V MN-major
+    return wait_bar_w(&bar[L::FULL + c % L::NST], (uint32_t)((c / L::NST) & 1), ctl, err);
+}
+
+// S of query tile U, issued by a warp of its own. The second tile starts when the first has its first
+// weights, which keeps the two tiles about half a step apart: in step they would wait for the MUFU and the
+// tensor core together and leave both idle together (10k prompt: 391 us in step, 352 us apart).
+template <int D, int U>
+__device__ __forceinline__ void s_loop(std::integral_constant<int, U> u, int myns, int ns, uint32_t tm, uint32_t sb,
+                                       uint64_t *bar, Ctl *ctl, uint32_t *err) {
+    using L = Layout<D>;
+    const uint32_t id_s = tc::make_idesc_bf16(TQ, STEP, 0, 0);  // both operands K-major
     const tc::Desc dq = tc::split_desc(tc::make_desc_sw128(sb + L::OFF_Q + u * L::TILE, 16, 1024));
     const tc::Desc dk = tc::split_desc(tc::make_desc_sw128(sb + L::OFF_KV, 16, 1024));
-    const tc::Desc dv = tc::split_desc(tc::make_desc_sw128(sb + L::OFF_KV, 16384, 1024));
-    // the ring holds K of steps 2 t and 2 t + 1 as tile 2 t, V of them as tile 2 t + 1
-    auto full = [&](int c) { return wait_bar_w(&bar[L::FULL + c % L::NST], (uint32_t)((c / L::NST) & 1), ctl, err); };
-    auto issue_s = [&](int j) {
+    bool ok = wait_bar_w(&bar[L::QFULL], 0, ctl, err);
+    if (ok && U == 1 && myns > 0) ok = wait_bar_w(&bar[L::PREADY], 0, ctl, err);
+    for (int j = 0; ok && j < myns; ++j) {
         const int c = j & ~1;
+        if (!(ok = ((j & 1) || ring_full<D>(bar, c, ctl, err)) &&
+                   (j == 0 || wait_bar_w(&bar[L::SFREE + u], (uint32_t)((j - 1) & 1), ctl, err))))
+            break;
+        tc::fence_after_sync();
         const uint32_t kb = (uint32_t)(c % L::NST) * L::TILE + (j & 1) * (STEP * 128);
-        const uint32_t ts = tm + L::TM_S + (2 * u + (j & 1)) * 64;
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
             const uint32_t off = (kk >> 2) * 16384 + (kk & 3) * 32;
-            tc::mma_bf16_off_w(ts, dq, off, dk, kb + off, id_s, kk > 0);
+            tc::mma_bf16_off_w(tm + L::TM_S + u * 64, dq, off, dk, kb + off, id_s, kk > 0);
         }
-        tc::mma_commit_w(&bar[L::SFULL + 2 * u + (j & 1)]);
+        tc::mma_commit_w(&bar[L::SFULL + u]);
         if ((j & 1) || j + 1 == myns) tc::mma_commit_w(&bar[L::EMPTY + c % L::NST]);
-    };
-    bool ok = wait_bar_w(&bar[L::QFULL], 0, ctl, err) && full(0);
-    if (ok) {
-        tc::fence_after_sync();
-        if (myns > 0) issue_s(0);
-        if (myns > 1) issue_s(1);
     }
-    for (int j = 0; ok && j < myns; ++j) {
-        const int b = j & 1, c = j | 1;
-        if (!(ok = full(c) && wait_bar_w(&bar[L::PREADY + 2 * u + b], (uint32_t)((j >> 1) & 1), ctl, err))) break;
-        tc::fence_after_sync();
-        const uint32_t vb = (uint32_t)(c % L::NST) * L::TILE + b * (STEP * 128);
-        const uint32_t ts = tm + L::TM_S + (2 * u + b) * 64;
-#pragma unroll
-        for (int kk = 0; kk < STEP / 16; ++kk)
-            tc::mma_bf16_ts_off_w(tm + L::TM_O + u * D, ts + 8 * kk, dv, vb + kk * 2048, id_o, (j > 0 || kk > 0) ? 1u : 0u);
-        tc::mma_commit_w(&bar[L::PVD + 2 * u + b]);
-        if (b || j + 1 == myns) tc::mma_commit_w(&bar[L::EMPTY + c % L::NST]);
-        if (j + 2 < myns) {
-            if (!(ok = full((j + 2) & ~1) && wait_bar_w(&bar[L::PVD + 2 * u + b], (uint32_t)((j >> 1) & 1), ctl, err))) break;
-            tc::fence_after_sync();
-            issue_s(j + 2);
-        }
-    }
-    // ring tiles that only the other query tile uses: freed as they come
-    for (int c = 2 * ((myns + 1) / 2); ok && c < 2 * ((ns + 1) / 2); ++c) {
-        ok = full(c);
+    for (int c = (myns + 1) / 2 * 2; ok && c < ns; c += 2) {  // K tiles that only the other query tile uses
+        ok = ring_full<D>(bar, c, ctl, err);
         if (ok && (threadIdx.x & 31) == 0) tc::mbar_arrive(&bar[L::EMPTY + c % L::NST]);
     }
-    tc::mma_commit_w(&bar[L::FIN]);
-    if ((threadIdx.x & 31) == 0) attn::drain_bar(&bar[L::FIN], 0);
-    __syncwarp();
+}
+
+// O of query tile u, issued by a warp of its own.
+template <int D, int U>
+__device__ __forceinline__ void pv_loop(std::integral_constant<int, U> u, int myns, int ns, uint32_t tm, uint32_t sb,
+                                        uint64_t *bar, Ctl *ctl, uint32_t *err) {
+    using L = Layout<D>;
+    const uint32_t id_o = tc::make_idesc_bf16(TQ, D, 0, 1);  // V MN-major
+    const tc::Desc dv = tc::split_desc(tc::make_desc_sw128(sb + L::OFF_KV, 16384, 1024));
+    bool ok = true;
+    for (int j = 0; ok && j < myns; ++j) {
+        const int b = j & 1, c = j | 1;
+        if (!(ok = (b || ring_full<D>(bar, c, ctl, err)) &&
+                   wait_bar_w(&bar[L::PREADY + 2 * u + b], (uint32_t)((j >> 1) & 1), ctl, err)))
+            break;
+        tc::fence_after_sync();
+        const uint32_t vb = (uint32_t)(c % L::NST) * L::TILE + b * (STEP * 128);
+#pragma unroll
+        for (int kk = 0; kk < STEP / 16; ++kk)
+            tc::mma_bf16_ts_off_w(tm + L::TM_O + u * D, tm + L::TM_P + (2 * u + b) * 32 + 8 * kk, dv, vb + kk * 2048, id_o,
+                                  (j > 0 || kk > 0) ? 1u : 0u);
+        tc::mma_commit_w(&bar[L::PVD + 2 * u + b]);
+        if (b || j + 1 == myns) tc::mma_commit_w(&bar[L::EMPTY + c % L::NST]);
+    }
+    for (int c = (myns + 1) / 2 * 2 + 1; ok && c <= ((ns - 1) | 1); c += 2) {  // V tiles that only the other query tile uses
+        ok = ring_full<D>(bar, c, ctl, err);
+        if (ok && (threadIdx.x & 31) == 0) tc::mbar_arrive(&bar[L::EMPTY + c % L::NST]);
+    }
 }
 
 template <int D, bool PREFIX>
@@ -153,7 +167,9 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     const uint32_t raw_base = tc::smem_u32(smem_raw);
     uint8_t *smem = smem_raw + ((1024u - (raw_base & 1023u)) & 1023u);
     const uint32_t sb = tc::smem_u32(smem);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    // (a shuffle, so that the compiler knows the roles' branches to be warp-uniform and keeps the product
+    // warps' operands in uniform registers)
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const int P = a.P;
 
     Item it;
@@ -203,14 +219,14 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     Ctl *ctl = reinterpret_cast<Ctl *>(smem + L::OFF_CTL);
     if (warp == W_MMA) tc::tmem_alloc(&ctl->tmem, 512);
     if (tid == W_LOAD * 32) {
-        for (int i = 0; i < L::NBAR; ++i) tc::mbar_init(&bar[i], (i >= L::PREADY && i < L::PREADY + 4) ? 128u : (i == L::FIN || (i >= L::EMPTY && i < L::SFULL)) ? 2u : 1u);
+        for (int i = 0; i < L::NBAR; ++i) tc::mbar_init(&bar[i], (i >= L::SFREE && i < L::PVD) ? 4u : i == L::FIN ? 4u : (i >= L::EMPTY && i < L::SFULL) ? 2u : 1u);
         ctl->abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
-    const uint32_t tm = ctl->tmem;
+    const uint32_t tm = __shfl_sync(0xffffffffu, ctl->tmem, 0);
 
     if (warp == W_LOAD) {
         if (lane == 0) {
@@ -263,10 +279,19 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             for (int i = std::max(c - L::NST, 0); i < c; ++i) attn::drain_bar(&bar[L::FULL + i % L::NST], (i / L::NST) & 1);
         }
         __syncwarp();
-    } else if (warp == W_MMA) {
-        mma_loop<D>(std::integral_constant<int, 0>(), it.ns0, ns, tm, sb, bar, ctl, a.err);
-    } else if (warp == W_MMA + 1) {
-        mma_loop<D>(std::integral_constant<int, 1>(), it.ns1, ns, tm, sb, bar, ctl, a.err);
+    } else if (warp >= W_MMA) {
+        if (warp == W_MMA)
+            s_loop<D>(std::integral_constant<int, 0>(), it.ns0, ns, tm, sb, bar, ctl, a.err);
+        else if (warp == W_MMA + 1)
+            s_loop<D>(std::integral_constant<int, 1>(), it.ns1, ns, tm, sb, bar, ctl, a.err);
+        else if (warp == W_MMA + 2)
+            pv_loop<D>(std::integral_constant<int, 0>(), it.ns0, ns, tm, sb, bar, ctl, a.err);
+        else
+            pv_loop<D>(std::integral_constant<int, 1>(), it.ns1, ns, tm, sb, bar, ctl, a.err);
+        // tensor memory may go once every product is done
+        tc::mma_commit_w(&bar[L::FIN]);
+        if (lane == 0) attn::drain_bar(&bar[L::FIN], 0);
+        __syncwarp();
     } else {
         // ---------------------------------------------------------------- softmax (one query row per thread)
         const int u = warp >> 2, r = tid & 127;
@@ -279,9 +304,9 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         float m_ref = -INFINITY, l = 0.f;
         bool ok = true;
         for (int j = 0; ok && j < myns; ++j) {
-            const int sbuf = 2 * u + (j & 1);
-            const uint32_t ts = tl + L::TM_S + sbuf * 64;
-            if (!(ok = wait_bar_w(&bar[L::SFULL + sbuf], (uint32_t)((j >> 1) & 1), ctl, a.err))) break;
+            const int pbuf = 2 * u + (j & 1);
+            const uint32_t ts = tl + L::TM_S + u * 64;
+            if (!(ok = wait_bar_w(&bar[L::SFULL + u], (uint32_t)(j & 1), ctl, a.err))) break;
             tc::fence_after_sync();
             // keys beyond this row's position, or beyond the prefix, are masked
             uint32_t s[2][32];
@@ -289,6 +314,9 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             attn::tmem_ld32x(ts + 32, s[1]);
             tc::tmem_wait_ld(s[0]);
             tc::tmem_wait_ld(s[1]);
+            tc::fence_before_sync();
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(&bar[L::SFREE + u]);  // the next S may overwrite these
             if (PREFIX ? it.keys - j * STEP < STEP : first - j * STEP < STEP - 1) {
                 const int lim = (PREFIX ? it.keys - 1 : pos) - j * STEP;
 #pragma unroll
@@ -344,7 +372,11 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                 ps[i & 1] = attn::add2(ps[i & 1], attn::pack2(p0, p1));
                 w[i] = tc::pack_bf16x2(p0, p1);
             }
-            tc::tmem_st32(ts, w);
+            if (j >= 2) {  // P's buffer: read two steps ago
+                if (!(ok = wait_bar_w(&bar[L::PVD + pbuf], (uint32_t)(((j >> 1) & 1) ^ 1), ctl, a.err))) break;
+                tc::fence_after_sync();
+            }
+            tc::tmem_st32(tl + L::TM_P + pbuf * 32, w);
             float a0, a1;
             attn::unpack2(attn::add2(ps[0], ps[1]), a0, a1);
             l += a0 + a1;
@@ -364,7 +396,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             }
             tc::tmem_st_wait();
             tc::fence_before_sync();
-            tc::mbar_arrive(&bar[L::PREADY + sbuf]);
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(&bar[L::PREADY + pbuf]);
         }
         if (ok && myns)
             ok = wait_bar_w(&bar[L::PVD + 2 * u + ((myns - 1) & 1)], (uint32_t)(((myns - 1) >> 1) & 1), ctl, a.err);
