@@ -61,9 +61,9 @@ struct Layout {
     static constexpr int NST = D == 128 ? 5 : 8;       // K and V tiles in the ring
     static constexpr uint32_t OFF_Q = 0, OFF_KV = 2 * TILE, OFF_BAR = OFF_KV + NST * TILE;
     // barriers: Q landed, ring full / empty, per query tile: S complete, S read; per query tile and P buffer
-    // (2 u + buffer): P written, O += P V done; all products done
+    // (2 u + buffer): P written, O += P V done; the first weights of tile 0; all products done
     static constexpr int QFULL = 0, FULL = 1, EMPTY = FULL + NST, SFULL = EMPTY + NST, SFREE = SFULL + 2,
-                         PREADY = SFREE + 2, PVD = PREADY + 4, FIN = PVD + 4, NBAR = FIN + 1;
+                         PREADY = SFREE + 2, PVD = PREADY + 4, START = PVD + 4, FIN = START + 1, NBAR = FIN + 1;
     static constexpr uint32_t OFF_CTL = OFF_BAR + 8 * NBAR;
     static constexpr uint32_t SMEM = OFF_CTL + 16 + 1024;
     // tensor memory columns: S of tile u at u * 64, P of tile u, buffer b at 128 + (2 u + b) * 32, O at 256 + u * D
@@ -89,8 +89,10 @@ __device__ __forceinline__ bool seqlens_bad(const AttnPrefill &a) {
 }
 
 // The ring holds K of steps 2 t and 2 t + 1 as tile 2 t, V of them as tile 2 t + 1. A tile is freed by two
-// arrivals, one for each query tile: the commit of that query tile's last product on it, or a plain arrival
-// where it has none.
+// arrivals, one for each query tile: the commit of that query tile's last product on it, or the loader's own
+// where it has none. A warp waits only for the tiles that it uses, K or V: a parity wait then is good only
+// because the tile before in the same stage (of the other kind) has certainly landed, as the same query
+// tile's earlier products read it.
 template <int D>
 __device__ __forceinline__ bool ring_full(uint64_t *bar, int c, Ctl *ctl, uint32_t *err) {
     using L = Layout<D>;
@@ -101,14 +103,14 @@ __device__ __forceinline__ bool ring_full(uint64_t *bar, int c, Ctl *ctl, uint32
 // weights, which keeps the two tiles about half a step apart: in step they would wait for the MUFU and the
 // tensor core together and leave both idle together (10k prompt: 391 us in step, 352 us apart).
 template <int D, int U>
-__device__ __forceinline__ void s_loop(std::integral_constant<int, U> u, int myns, int ns, uint32_t tm, uint32_t sb,
+__device__ __forceinline__ void s_loop(std::integral_constant<int, U> u, int myns, uint32_t tm, uint32_t sb,
                                        uint64_t *bar, Ctl *ctl, uint32_t *err) {
     using L = Layout<D>;
     const uint32_t id_s = tc::make_idesc_bf16(TQ, STEP, 0, 0);  // both operands K-major
     const tc::Desc dq = tc::split_desc(tc::make_desc_sw128(sb + L::OFF_Q + u * L::TILE, 16, 1024));
     const tc::Desc dk = tc::split_desc(tc::make_desc_sw128(sb + L::OFF_KV, 16, 1024));
     bool ok = wait_bar_w(&bar[L::QFULL], 0, ctl, err);
-    if (ok && U == 1 && myns > 0) ok = wait_bar_w(&bar[L::PREADY], 0, ctl, err);
+    if (ok && U == 1 && myns > 0) ok = wait_bar_w(&bar[L::START], 0, ctl, err);
     for (int j = 0; ok && j < myns; ++j) {
         const int c = j & ~1;
         if (!(ok = ((j & 1) || ring_full<D>(bar, c, ctl, err)) &&
@@ -124,15 +126,11 @@ __device__ __forceinline__ void s_loop(std::integral_constant<int, U> u, int myn
         tc::mma_commit_w(&bar[L::SFULL + u]);
         if ((j & 1) || j + 1 == myns) tc::mma_commit_w(&bar[L::EMPTY + c % L::NST]);
     }
-    for (int c = (myns + 1) / 2 * 2; ok && c < ns; c += 2) {  // K tiles that only the other query tile uses
-        ok = ring_full<D>(bar, c, ctl, err);
-        if (ok && (threadIdx.x & 31) == 0) tc::mbar_arrive(&bar[L::EMPTY + c % L::NST]);
-    }
 }
 
 // O of query tile u, issued by a warp of its own.
 template <int D, int U>
-__device__ __forceinline__ void pv_loop(std::integral_constant<int, U> u, int myns, int ns, uint32_t tm, uint32_t sb,
+__device__ __forceinline__ void pv_loop(std::integral_constant<int, U> u, int myns, uint32_t tm, uint32_t sb,
                                         uint64_t *bar, Ctl *ctl, uint32_t *err) {
     using L = Layout<D>;
     const uint32_t id_o = tc::make_idesc_bf16(TQ, D, 0, 1);  // V MN-major
@@ -151,10 +149,6 @@ __device__ __forceinline__ void pv_loop(std::integral_constant<int, U> u, int my
                                   (j > 0 || kk > 0) ? 1u : 0u);
         tc::mma_commit_w(&bar[L::PVD + 2 * u + b]);
         if (b || j + 1 == myns) tc::mma_commit_w(&bar[L::EMPTY + c % L::NST]);
-    }
-    for (int c = (myns + 1) / 2 * 2 + 1; ok && c <= ((ns - 1) | 1); c += 2) {  // V tiles that only the other query tile uses
-        ok = ring_full<D>(bar, c, ctl, err);
-        if (ok && (threadIdx.x & 31) == 0) tc::mbar_arrive(&bar[L::EMPTY + c % L::NST]);
     }
 }
 
@@ -219,7 +213,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     Ctl *ctl = reinterpret_cast<Ctl *>(smem + L::OFF_CTL);
     if (warp == W_MMA) tc::tmem_alloc(&ctl->tmem, 512);
     if (tid == W_LOAD * 32) {
-        for (int i = 0; i < L::NBAR; ++i) tc::mbar_init(&bar[i], (i >= L::SFREE && i < L::PVD) ? 4u : i == L::FIN ? 4u : (i >= L::EMPTY && i < L::SFULL) ? 2u : 1u);
+        for (int i = 0; i < L::NBAR; ++i) tc::mbar_init(&bar[i], ((i >= L::SFREE && i < L::PVD) || i == L::START) ? 4u : i == L::FIN ? 4u : (i >= L::EMPTY && i < L::SFULL) ? 2u : 1u);
         ctl->abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -258,7 +252,11 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             for (int kv = 0; kv < 2; ++kv, ++c) {
                 const int st = c % L::NST;
                 if (c >= L::NST && !(ok = wait_bar_w(&bar[L::EMPTY + st], (uint32_t)((c / L::NST - 1) & 1), ctl, a.err))) break;
-                if (lane == 0) tc::mbar_arrive_expect_tx(&bar[L::FULL + st], L::TILE);
+                if (lane == 0) {
+                    if (2 * j >= it.ns0) tc::mbar_arrive(&bar[L::EMPTY + st]);  // a query tile that does not use it
+                    if (2 * j >= it.ns1) tc::mbar_arrive(&bar[L::EMPTY + st]);
+                    tc::mbar_arrive_expect_tx(&bar[L::FULL + st], L::TILE);
+                }
                 __syncwarp();
                 const CUtensorMap *map = kv ? &tm_v : &tm_k;
                 const uint32_t dst = sb + L::OFF_KV + st * L::TILE + lane * rows * 128;
@@ -281,13 +279,13 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         __syncwarp();
     } else if (warp >= W_MMA) {
         if (warp == W_MMA)
-            s_loop<D>(std::integral_constant<int, 0>(), it.ns0, ns, tm, sb, bar, ctl, a.err);
+            s_loop<D>(std::integral_constant<int, 0>(), it.ns0, tm, sb, bar, ctl, a.err);
         else if (warp == W_MMA + 1)
-            s_loop<D>(std::integral_constant<int, 1>(), it.ns1, ns, tm, sb, bar, ctl, a.err);
+            s_loop<D>(std::integral_constant<int, 1>(), it.ns1, tm, sb, bar, ctl, a.err);
         else if (warp == W_MMA + 2)
-            pv_loop<D>(std::integral_constant<int, 0>(), it.ns0, ns, tm, sb, bar, ctl, a.err);
+            pv_loop<D>(std::integral_constant<int, 0>(), it.ns0, tm, sb, bar, ctl, a.err);
         else
-            pv_loop<D>(std::integral_constant<int, 1>(), it.ns1, ns, tm, sb, bar, ctl, a.err);
+            pv_loop<D>(std::integral_constant<int, 1>(), it.ns1, tm, sb, bar, ctl, a.err);
         // tensor memory may go once every product is done
         tc::mma_commit_w(&bar[L::FIN]);
         if (lane == 0) attn::drain_bar(&bar[L::FIN], 0);
@@ -397,7 +395,10 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             tc::tmem_st_wait();
             tc::fence_before_sync();
             __syncwarp();
-            if (lane == 0) tc::mbar_arrive(&bar[L::PREADY + pbuf]);
+            if (lane == 0) {
+                tc::mbar_arrive(&bar[L::PREADY + pbuf]);
+                if (u == 0 && j == 0) tc::mbar_arrive(&bar[L::START]);  // (PREADY's phases come round; this one's does not)
+            }
         }
         if (ok && myns)
             ok = wait_bar_w(&bar[L::PVD + 2 * u + ((myns - 1) & 1)], (uint32_t)(((myns - 1) >> 1) & 1), ctl, a.err);

@@ -161,6 +161,36 @@ def test_prefill_tile_edges(lens):
     close(o, ref, attn_tol(ref, a, q, k, 128, max(lens)))
 
 
+@pytest.mark.parametrize("Hq,Hkv", [(8, 8), (16, 4)])
+def test_prefill_many_short_prompts(Hq, Hkv):
+    """Thousands of blocks whose first query tile has only a few steps of keys: no wait gives up, and
+    equal prompts give equal outputs whichever block computes them."""
+    gen = torch.Generator().manual_seed(13)
+    lens = [256, 140, 200, 256] * 40
+    q, k, v, _ = prompt(gen, lens[:4], Hq, Hkv, 128)
+    q, k, v = (x.repeat(40, 1, 1).cuda() for x in (q, k, v[:, Hq + Hkv:]))
+    cu = torch.tensor(np.concatenate([[0], np.cumsum(lens)]), dtype=torch.int32).cuda()
+    o = gdn.attn_prefill(q, k, v, cu, max_len=256, check=True)
+    assert torch.isfinite(o).all()
+    assert torch.equal(o.view(40, -1), o[:sum(lens[:4])].reshape(1, -1).expand(40, -1))
+
+
+@pytest.mark.parametrize("G", [1, 4])
+def test_prefill_long_sequences_that_leave_a_query_tile_empty(G):
+    """Lengths whose last block has rows in its first query tile only (or few steps less in it), over
+    many key tiles and sequences: key tiles that one query tile alone uses are freed in their turn."""
+    gen = torch.Generator().manual_seed(14)
+    lens = [4032 + 15, 3968 + 21, 832 + 27, 1984 + 6, 3904 + 30, 130, 4096 - 127]
+    q, k, v, cu = prompt(gen, lens, 4 * G, 4, 128)
+    q, k, v, cu = q.cuda(), k.cuda(), v[:, 4 * G + 4:].contiguous().cuda(), cu.cuda()
+    want = gdn.attn_prefill(q, k, v, cu, max_len=max(lens), check=True)
+    for _ in range(20):
+        assert torch.equal(gdn.attn_prefill(q, k, v, cu, max_len=max(lens), check=True), want)
+    b = sum(lens[:2]) + lens[2]
+    ref, a = al.prompt_attention(q[b - lens[2]:b], k[b - lens[2]:b], v[b - lens[2]:b], [lens[2]])
+    close(want[b - lens[2]:b], ref, attn_tol(ref, a, q, k, 128, lens[2]))
+
+
 @pytest.mark.parametrize("trend", ["rising", "falling", "spikes"])
 @pytest.mark.parametrize("d", [64, 128])
 def test_prefill_moving_maximum(trend, d):
