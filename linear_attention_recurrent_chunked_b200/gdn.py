@@ -94,32 +94,6 @@ def _stream() -> ctypes.c_void_p:
     return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
 
 
-def _at(t: Optional[torch.Tensor]):
-    return None if t is None else t.data_ptr()
-
-
-def _stream_of(device) -> int:
-    return torch.cuda.current_stream(device).cuda_stream
-
-
-class _Nothing:
-    def __enter__(self):
-        return None
-
-    def __exit__(self, *exc):
-        return False
-
-
-_NOTHING = _Nothing()
-
-
-def _on(device):
-    """Makes the tensors' device the current one for a call, where it is not."""
-    if device.type != "cuda":
-        raise GdnError(1, "tensors must be on a CUDA device (no CPU path)")
-    return _NOTHING if device.index == torch.cuda.current_device() else torch.cuda.device(device)
-
-
 def _need_cuda(*ts):
     for t in ts:
         if t is not None:
@@ -261,43 +235,77 @@ def attn_fwd(q, k, v, cu_seqlens=None, N: Optional[int] = None, max_len: Optiona
     return o
 
 
-def _heads(name, t, device, dtype, H=None, d=None):
-    """Token stride of a [T, H, d] tensor whose tokens are contiguous (the heads of one token may be a
-    slice of a wider row); raises unless it is one, on `device` and of type `dtype`."""
-    if t.dim() != 3 or (H is not None and t.shape[1] != H) or (d is not None and t.shape[2] != d):
-        raise GdnError(2, "%s has shape %s" % (name, tuple(t.shape)))
+def _refuse(name, t, index, dtype, shape):
+    """Says what is wrong with a tensor that one of the checks below did not accept."""
+    if not isinstance(t, torch.Tensor):
+        raise GdnError(1, "%s is %r, not a tensor" % (name, type(t).__name__))
     if t.dtype != dtype:
         raise GdnError(3, "%s is %s, not %s" % (name, t.dtype, dtype))
-    if t.device != device or not t.is_cuda:
-        raise GdnError(1, "%s is on %s (all tensors must be on one CUDA device)" % (name, t.device))
-    st = t.stride()
-    if t.numel() and ((st[2] != 1 and t.shape[2] != 1) or (st[1] != t.shape[2] and t.shape[1] != 1)):
-        raise GdnError(2, "%s: the heads of a token must be contiguous" % name)
-    return st[0] if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+    if t.dim() != len(shape) or any(n is not None and n != m for n, m in zip(shape, t.shape)):
+        raise GdnError(2, "%s has shape %s, not %s" % (name, tuple(t.shape), tuple("*" if n is None else n for n in shape)))
+    if not t.is_cuda or t.get_device() != index:
+        raise GdnError(1, "%s is on %s (all tensors must be on one CUDA device; no CPU path)" % (name, t.device))
+    raise GdnError(2, "%s must be contiguous%s" % (name, " within a token" if len(shape) == 3 else ""))
 
 
-def _flat(name, t, device, dtype, shape):
-    """Checks a contiguous tensor of the given type and shape."""
-    if t.dtype != dtype:
-        raise GdnError(3, "%s is %s, not %s" % (name, t.dtype, dtype))
-    if tuple(t.shape) != shape:
-        raise GdnError(2, "%s has shape %s, not %s" % (name, tuple(t.shape), shape))
-    if t.device != device:
-        raise GdnError(1, "%s is on %s (all tensors must be on one CUDA device)" % (name, t.device))
-    if not t.is_contiguous():
-        raise GdnError(2, "%s must be contiguous" % name)
+def _flat(name, t, index, dtype, shape):
+    """Address of a contiguous tensor on device `index` with this type and shape."""
+    if t.dtype is dtype and t.shape == shape and t.get_device() == index and t.is_contiguous():
+        return t.data_ptr()
+    _refuse(name, t, index, dtype, shape)
 
 
-def _call_ws(nbytes: int, device, workspace):
-    """The caller's workspace, or the cached one of this device and stream; while a graph is being
-    captured a fresh one, so that the graph keeps memory of its own."""
-    if workspace is not None:
-        if workspace.device != device or not workspace.is_contiguous():
-            raise GdnError(6, "workspace must be a contiguous tensor on the inputs' device")
-        return workspace
-    if torch.cuda.is_current_stream_capturing():
-        return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
-    return _workspace(nbytes, device)
+def _heads(name, t, index, dtype, T, H, d):
+    """Address and token stride of a [T, H, d] tensor whose tokens are contiguous: a token's heads may be
+    a slice of a wider row."""
+    if t.dtype is dtype and t.shape == (T, H, d) and t.get_device() == index:
+        st, s1, s2 = t.stride()
+        if (s2 == 1 and (s1 == d or H == 1)) or not T:
+            return t.data_ptr(), st if T > 1 else H * d
+    _refuse(name, t, index, dtype, (T, H, d))
+
+
+def _index(name, t):
+    """The device that a call runs on: its first tensor's."""
+    if t.dim() != 3 or not t.is_cuda:
+        _refuse(name, t, 0, t.dtype, (None, None, None))
+    return t.get_device()
+
+
+def _stream_and_ws(index, nbytes, workspace):
+    """The current stream of a device, and a workspace: the caller's, or the cached one of this device
+    and stream, or while a graph is being captured a fresh one, so that the graph keeps memory of its own."""
+    stream = torch._C._cuda_getCurrentRawStream(index)
+    if workspace is None:
+        if torch.cuda.is_current_stream_capturing():
+            workspace = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=torch.device("cuda", index))
+        else:
+            workspace = _ws_cache.get((index, stream))
+            if workspace is None or workspace.numel() < nbytes:
+                workspace = _workspace(nbytes, torch.device("cuda", index))
+        return stream, workspace, workspace.numel()
+    if not workspace.is_contiguous() or workspace.get_device() != index:
+        raise GdnError(6, "workspace must be a contiguous tensor on the inputs' device")
+    return stream, workspace, workspace.numel() * workspace.element_size()
+
+
+class _Nothing:
+    def __enter__(self):
+        return None
+
+    def __exit__(self, *exc):
+        return False
+
+
+_NOTHING = _Nothing()
+
+
+def _on(index):
+    """Makes the tensors' device the current one for a call, where it is not."""
+    return _NOTHING if index == torch.cuda.current_device() else torch.cuda.device(index)
+
+
+_BF16, _I32, _FP32 = torch.bfloat16, torch.int32, torch.float32
 
 
 def qk_norm_rope(q, k, wq, wk, positions, v=None, rot: Optional[int] = None, base: float = 10000.0, eps: float = 1e-6,
@@ -310,51 +318,48 @@ def qk_norm_rope(q, k, wq, wk, positions, v=None, rot: Optional[int] = None, bas
     [pages,Hkv,page_size,d]. Returns (q_out, k_out); k_out is None with want_k=False, for callers that
     read the keys from the cache."""
     lib = load_library()
-    dev, dtype = q.device, q.dtype
+    dtype = q.dtype
     if dtype not in _DTYPE:
         raise GdnError(3, "q is %s (float32 or bfloat16)" % dtype)
-    q_stride = _heads("q", q, dev, dtype)
+    index = _index("q", q)
     T, Hq, d = q.shape
-    k_stride = _heads("k", k, dev, dtype, d=d)
-    Hkv = k.shape[1]
-    if k.shape[0] != T:
-        raise GdnError(2, "k has %d tokens, q %d" % (k.shape[0], T))
-    v_stride = 0
-    pages, page_size = 0, 0
+    Hkv = k.shape[1] if k.dim() == 3 else -1
+    pq, q_stride = _heads("q", q, index, dtype, T, Hq, d)
+    pk, k_stride = _heads("k", k, index, dtype, T, Hkv, d)
+    pv = pkc = pvc = ps = None
+    v_stride = pages = page_size = 0
     if slots is not None:
         if v is None or k_cache is None or v_cache is None:
             raise GdnError(1, "slots needs v, k_cache and v_cache")
-        v_stride = _heads("v", v, dev, dtype, Hkv, d)
-        if v.shape[0] != T:
-            raise GdnError(2, "v has %d tokens, q %d" % (v.shape[0], T))
-        if k_cache.dim() != 4:
-            raise GdnError(2, "k_cache has shape %s" % (tuple(k_cache.shape),))
-        pages, page_size = k_cache.shape[0], k_cache.shape[2]
-        _flat("k_cache", k_cache, dev, dtype, (pages, Hkv, page_size, d))
-        _flat("v_cache", v_cache, dev, dtype, (pages, Hkv, page_size, d))
-        _flat("slots", slots, dev, torch.int32, (T,))
-    rot = d if rot is None else rot
-    for name, w in (("wq", wq), ("wk", wk)):
-        if w is not None:
-            _flat(name, w, dev, torch.float32, (d,))
-    if positions is not None:
-        _flat("positions", positions, dev, torch.int32, (T,))
-    with _on(dev):
+        pv, v_stride = _heads("v", v, index, dtype, T, Hkv, d)
+        shape = k_cache.shape
+        if len(shape) != 4 or shape[1] != Hkv or shape[3] != d:
+            _refuse("k_cache", k_cache, index, dtype, (None, Hkv, None, d))
+        pages, page_size = shape[0], shape[2]
+        pkc = _flat("k_cache", k_cache, index, dtype, shape)
+        pvc = _flat("v_cache", v_cache, index, dtype, shape)
+        ps = _flat("slots", slots, index, _I32, (T,))
+    pwq = None if wq is None else _flat("wq", wq, index, _FP32, (d,))
+    pwk = None if wk is None else _flat("wk", wk, index, _FP32, (d,))
+    pp = None if positions is None else _flat("positions", positions, index, _I32, (T,))
+    with _on(index):
         if q_out is None:
-            q_out = torch.empty((T, Hq, d), dtype=dtype, device=dev)
+            q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
+            pqo = q_out.data_ptr()
         else:
-            _flat("q_out", q_out, dev, dtype, (T, Hq, d))
+            pqo = _flat("q_out", q_out, index, dtype, (T, Hq, d))
+        pko = None
         if k_out is not None:
-            _flat("k_out", k_out, dev, dtype, (T, Hkv, d))
+            pko = _flat("k_out", k_out, index, dtype, (T, Hkv, d))
         elif want_k:
-            k_out = torch.empty((T, Hkv, d), dtype=dtype, device=dev)
-        ws = _call_ws(256, dev, workspace)
-        _check(lib.gdn_qk_norm_rope(_at(q), q_stride, _at(k), k_stride, _at(v) if slots is not None else None, v_stride,
-                                    _at(wq), _at(wk), eps, _at(positions), T, Hq, Hkv, d, rot, base, _DTYPE[dtype],
-                                    _at(q_out), _at(k_out), _at(k_cache), _at(v_cache), _at(slots), pages, page_size,
-                                    ws.data_ptr(), ws.numel() * ws.element_size(), _stream_of(dev)))
+            k_out = torch.empty_like(k, memory_format=torch.contiguous_format)
+            pko = k_out.data_ptr()
+        stream, ws, ws_bytes = _stream_and_ws(index, 256, workspace)
+        _check(lib.gdn_qk_norm_rope(pq, q_stride, pk, k_stride, pv, v_stride, pwq, pwk, eps, pp, T, Hq, Hkv, d,
+                                    d if rot is None else rot, base, _DTYPE[dtype], pqo, pko, pkc, pvc, ps, pages, page_size,
+                                    ws.data_ptr(), ws_bytes, stream))
         if check:
-            _check(lib.gdn_chunk_fwd_check(_ptr(ws), ws.numel(), _stream()))
+            _check(lib.gdn_chunk_fwd_check(ws.data_ptr(), ws_bytes, stream))
     return q_out, k_out
 
 
@@ -365,35 +370,37 @@ def attn_prefill(q, k, v, cu_seqlens=None, N: Optional[int] = None, max_len: Opt
     (N equal sequences, N from ``N``, else 1); max_len bounds the lengths (required with cu_seqlens);
     scale <= 0 means 1 / sqrt(d). Returns o [T,Hq,d]."""
     lib = load_library()
-    dev = q.device
-    q_stride = _heads("q", q, dev, torch.bfloat16)
+    if q.dtype is not _BF16:
+        raise GdnError(3, "q is %s, not %s" % (q.dtype, _BF16))
+    index = _index("q", q)
     T, Hq, d = q.shape
-    k_stride = _heads("k", k, dev, torch.bfloat16, d=d)
-    Hkv = k.shape[1]
-    v_stride = _heads("v", v, dev, torch.bfloat16, Hkv, d)
-    if k.shape[0] != T or v.shape[0] != T:
-        raise GdnError(2, "q, k and v have %d, %d and %d tokens" % (T, k.shape[0], v.shape[0]))
+    Hkv = k.shape[1] if k.dim() == 3 else -1
+    pq, q_stride = _heads("q", q, index, _BF16, T, Hq, d)
+    pk, k_stride = _heads("k", k, index, _BF16, T, Hkv, d)
+    pv, v_stride = _heads("v", v, index, _BF16, T, Hkv, d)
+    pcu = None
     if cu_seqlens is not None:
         N = cu_seqlens.numel() - 1
-        _flat("cu_seqlens", cu_seqlens, dev, torch.int32, (N + 1,))
+        pcu = _flat("cu_seqlens", cu_seqlens, index, _I32, (N + 1,))
         if max_len is None:
             raise GdnError(2, "max_len is required with cu_seqlens")
+        max_len = min(max_len, T)
     else:
         N = 1 if N is None else N
         if N < 1:
             raise GdnError(2, "N=%d must be >= 1" % N)
         max_len = T // N
-    with _on(dev):
+    with _on(index):
         if o is None:
-            o = torch.empty((T, Hq, d), dtype=torch.bfloat16, device=dev)
+            o = torch.empty_like(q, memory_format=torch.contiguous_format)
+            po = o.data_ptr()
         else:
-            _flat("o", o, dev, torch.bfloat16, (T, Hq, d))
-        ws = _call_ws(256, dev, workspace)
-        _check(lib.gdn_attn_prefill(_at(q), q_stride, _at(k), k_stride, _at(v), v_stride, _at(cu_seqlens), N, T, Hq, Hkv,
-                                    d, min(max_len, T), scale, GDN_BF16, _at(o), ws.data_ptr(),
-                                    ws.numel() * ws.element_size(), _stream_of(dev)))
+            po = _flat("o", o, index, _BF16, (T, Hq, d))
+        stream, ws, ws_bytes = _stream_and_ws(index, 256, workspace)
+        _check(lib.gdn_attn_prefill(pq, q_stride, pk, k_stride, pv, v_stride, pcu, N, T, Hq, Hkv, d, max_len, scale, GDN_BF16,
+                                    po, ws.data_ptr(), ws_bytes, stream))
         if check:
-            _check(lib.gdn_chunk_fwd_check(_ptr(ws), ws.numel(), _stream()))
+            _check(lib.gdn_chunk_fwd_check(ws.data_ptr(), ws_bytes, stream))
     return o
 
 
@@ -403,35 +410,46 @@ def attn_decode(q, k_cache, v_cache, page_table, lens, prefix_pages=None, prefix
     bf16, k_cache, v_cache [pages,Hkv,page_size,d] bf16, page_table [B,max_pages] int32, lens [B] int32;
     prefix_pages [n] int32 and prefix_len: a prefix that all sequences share. Returns o [B,Hq,d]."""
     lib = load_library()
-    dev = q.device
-    if q.dim() != 3 or k_cache.dim() != 4 or page_table.dim() != 2:
-        raise GdnError(2, "q, k_cache, page_table have shapes %s, %s, %s" % (tuple(q.shape), tuple(k_cache.shape),
-                                                                              tuple(page_table.shape)))
-    B, Hq, d = q.shape
-    pages, Hkv, page_size, _ = k_cache.shape
-    _flat("q", q, dev, torch.bfloat16, (B, Hq, d))
-    _flat("k_cache", k_cache, dev, torch.bfloat16, (pages, Hkv, page_size, d))
-    _flat("v_cache", v_cache, dev, torch.bfloat16, (pages, Hkv, page_size, d))
-    _flat("page_table", page_table, dev, torch.int32, (B, page_table.shape[1]))
-    _flat("lens", lens, dev, torch.int32, (B,))
+    if q.dtype is not _BF16:
+        raise GdnError(3, "q is %s, not %s" % (q.dtype, _BF16))
+    shape, table = k_cache.shape, page_table.shape
+    B, Hq, d = q.shape if q.dim() == 3 else (-1, -1, -1)
+    if len(shape) != 4 or shape[3] != d:
+        _refuse("k_cache", k_cache, 0, _BF16, (None, None, None, d))
+    if len(table) != 2:
+        _refuse("page_table", page_table, 0, _I32, (B, None))
+    pages, Hkv, page_size, _ = shape
+    if v_cache.shape != shape:
+        _refuse("v_cache", v_cache, 0, _BF16, shape)
+    if lens.shape != (B,):
+        _refuse("lens", lens, 0, _I32, (B,))
+    if page_table.dtype is not _I32:
+        _refuse("page_table", page_table, 0, _I32, (B, None))
     if prefix_len:
         if prefix_pages is None:
             raise GdnError(1, "prefix_len needs prefix_pages")
-        _flat("prefix_pages", prefix_pages, dev, torch.int32, (prefix_pages.numel(),))
         if prefix_len > prefix_pages.numel() * page_size:
             raise GdnError(2, "prefix_len=%d exceeds the %d prefix pages" % (prefix_len, prefix_pages.numel()))
-    with _on(dev):
+    if not q.is_contiguous():
+        raise GdnError(2, "q must be contiguous")
+    index = _index("q", q)
+    pq = _flat("q", q, index, _BF16, (B, Hq, d))
+    pk = _flat("k_cache", k_cache, index, _BF16, shape)
+    pv = _flat("v_cache", v_cache, index, _BF16, shape)
+    pt = _flat("page_table", page_table, index, _I32, (B, table[1]))
+    pl = _flat("lens", lens, index, _I32, (B,))
+    pp = _flat("prefix_pages", prefix_pages, index, _I32, (prefix_pages.numel(),)) if prefix_len else None
+    with _on(index):
         if o is None:
-            o = torch.empty((B, Hq, d), dtype=torch.bfloat16, device=dev)
+            o = torch.empty_like(q)
+            po = o.data_ptr()
         else:
-            _flat("o", o, dev, torch.bfloat16, (B, Hq, d))
-        ws = _call_ws(lib.gdn_attn_decode_workspace_size(B, Hq, Hkv, d, prefix_len), dev, workspace)
-        _check(lib.gdn_attn_decode(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), pages, page_size,
-                                   page_table.data_ptr(), page_table.shape[1], lens.data_ptr(),
-                                   _at(prefix_pages) if prefix_len else None, prefix_len, B, Hq, Hkv, d, scale, GDN_BF16,
-                                   o.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size(), _stream_of(dev)))
+            po = _flat("o", o, index, _BF16, (B, Hq, d))
+        stream, ws, ws_bytes = _stream_and_ws(index, lib.gdn_attn_decode_workspace_size(B, Hq, Hkv, d, prefix_len), workspace)
+        _check(lib.gdn_attn_decode(pq, pk, pv, pages, page_size, pt, table[1], pl, pp, prefix_len, B, Hq, Hkv, d, scale,
+                                   GDN_BF16, po, ws.data_ptr(), ws_bytes, stream))
         if check:
-            _check(lib.gdn_chunk_fwd_check(_ptr(ws), ws.numel(), _stream()))
+            _check(lib.gdn_chunk_fwd_check(ws.data_ptr(), ws_bytes, stream))
     return o
 
 
