@@ -9,15 +9,16 @@
 // give equal bits.
 //
 // Own keys (k_attn_decode). Bound: HBM, each key and value row is read once for the G query heads of
-// its key head (G <= 16: at most 16 flops a byte). The work is cut into units of 128 keys of one
-// (sequence, key head), numbered sequence by sequence; each CTA takes an equal run of consecutive units
-// whatever the lengths are, so ragged batches and single long sequences alike fill the GPU. A run cuts
-// at most its first and last (sequence, head) short; those pieces go to two slots of the CTA, all
-// others are finished in place. In a unit a warp owns 16 keys, brought by 16-byte asynchronous copies into
-// a ring of its own that runs ahead across (sequence, head) borders. The products are
-// S^T = K Q^T and O^T = V^T P^T on m16n8k16 tensor instructions: the 16 keys (or 16 of the d columns)
-// are the rows and the heads the 8 columns, so a group of up to 8 heads wastes nothing on padding rows,
-// which a 128-row tile would; at these few flops a byte the memory stays the bound.
+// its key head (G <= 16: at most 16 flops a byte). The work is cut into steps of 16 keys of one (sequence,
+// key head), numbered sequence by sequence; each warp of one resident grid takes an equal run of
+// consecutive steps whatever the lengths are, so ragged batches and single long sequences alike fill the
+// GPU, and a warp never waits for another while keys are left. A step's rows (8 KB for d = 128) come by
+// TMA, four 2 KB boxes, into a ring of the warp's own that runs ahead across (sequence, head) borders
+// (by 16-byte asynchronous copies a step took 750 cycles to ask for, as long as all of its arithmetic). The products are S^T = K Q^T and O^T = V^T P^T on m16n8k16 tensor instructions: the 16 keys (or
+// 16 of the d columns) are the rows and the heads the 8 columns, so a group of up to 8 heads wastes
+// nothing on padding rows, which a 128-row tile would; at these few flops a byte the memory stays the
+// bound. A run cuts at most its first and last (sequence, head) short: those pieces are joined over the
+// CTA's warps once at the end, and what even the CTA's run cuts short goes to the CTA's two slots.
 //
 // The prefix runs in the prompt kernel (attn_prefill.cu) without a mask, all sequences' query heads of a
 // key head as rows of one tile, so its keys are read once per 256 rows and not once per sequence.
@@ -33,20 +34,23 @@ namespace gdn {
 namespace {
 
 using bf16 = __nv_bfloat16;
+using attn::Ctl;
 constexpr int kWarps = 8, kThreads = kWarps * 32;
-constexpr int kStep = 16;                // keys of a warp in a unit
-constexpr int kUnit = kWarps * kStep;    // keys of a unit
+constexpr int kStep = 16;                // keys of a step
+constexpr int kRuns = kDecodeCtas * kWarps;
 constexpr float kRescale = 8.f;          // log2 units: how far the true maximum may run ahead of the reference
 
-template <int D>
+template <int D, int NT>
 struct Smem {
-    static constexpr int NST = 3 * 128 / D;              // ring stages of a warp
-    static constexpr uint32_t HALF = kStep * D * 2;      // K, then V, of a stage
-    static constexpr uint32_t RING = NST * 2 * HALF;     // per warp
-    static constexpr int LD = D + 4;                     // padded row of the merge buffer
-    static constexpr uint32_t OFF_MRG = kWarps * RING;
-    static constexpr uint32_t OFF_ML = OFF_MRG + kWarps * 8 * LD * 4;
-    static constexpr uint32_t TOTAL = OFF_ML + kWarps * 8 * 8;
+    static constexpr int NST = (NT == 1 ? 3 : 2) * 128 / D;  // ring stages of a warp
+    static constexpr uint32_t HALF = kStep * D * 2;          // K, then V, of a stage
+    static constexpr uint32_t RING = NST * 2 * HALF;         // per warp
+    static constexpr int LD = D + 4;                         // padded row of a piece
+    static constexpr uint32_t PIECE = NT * 8 * LD * 4;       // O of a piece (a warp's last one goes over its ring)
+    static constexpr uint32_t OFF_FIRST = kWarps * RING;
+    static constexpr uint32_t OFF_ML = OFF_FIRST + kWarps * PIECE;
+    static constexpr uint32_t TOTAL = OFF_ML + kWarps * 2 * NT * 8 * 8;
+    static_assert(PIECE <= RING && kWarps * PIECE >= kThreads * 8, "");
 };
 
 __device__ __forceinline__ void ldmatrix4(uint32_t addr, uint32_t (&r)[4]) {
@@ -72,33 +76,56 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
 __device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void grid_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 __device__ __forceinline__ int length_of(const AttnDecode &a, int b) {
     return min(max(a.lens[b], 0), a.max_pages << a.page_log);  // max_pages << page_log is at most 2^30
 }
-__device__ __forceinline__ int units_of(int len) { return (len + kUnit - 1) / kUnit; }
+__device__ __forceinline__ int steps_of(int len) { return (len + kStep - 1) / kStep; }
 
-// The run of units of CTA c is [first_unit(c), first_unit(c + 1)). With fewer units than CTAs each of the
-// first `units` CTAs has one, so that the pieces of a (sequence, head) always lie in consecutive CTAs.
-__device__ __forceinline__ int64_t first_unit(int64_t units, int c) {
-    return units < kDecodeCtas ? min((int64_t)c, units) : units * c / kDecodeCtas;
+// The run of steps of warp w of the grid is [first_step(w), first_step(w + 1)). With fewer steps than warps
+// each of the first warps has one, so that the pieces of a (sequence, head) always lie in consecutive CTAs.
+__device__ __forceinline__ int first_step(int steps, int w) {  // (steps are below 2^31, which the call checks)
+    return steps < kRuns ? min(w, steps) : (int)((uint64_t)steps * (uint32_t)w / kRuns);
 }
-// The CTA whose run holds unit x.
-__device__ __forceinline__ int cta_of(int64_t units, int64_t x) {
-    if (units < kDecodeCtas) return (int)x;
-    int c = (int)(x * kDecodeCtas / units);
-    while (c > 0 && first_unit(units, c) > x) --c;
-    while (first_unit(units, c + 1) <= x) ++c;
-    return c;
+// The CTA whose warps' runs hold step x.
+__device__ __forceinline__ int cta_of(int steps, int x) {
+    if (steps < kRuns) return x / kWarps;
+    int w = (int)((float)x / (float)steps * kRuns);  // about
+    w = min(max(w, 0), kRuns - 1);
+    while (first_step(steps, w) > x) --w;
+    while (first_step(steps, w + 1) <= x) ++w;
+    return w / kWarps;
 }
 
-// A place in a CTA's run: unit `chunk` of the `n` units of (sequence b, key head h).
+// Q^T as the second operand of S^T = K Q^T: of head g (lane / 4) of the group at q, words lane % 4 of each
+// 8-column chunk. Loaded as whole chunks, 16 bytes a lane, and transposed within the four lanes of a head: as
+// words, the many warps that start on one head together would ask L2 for its sectors 8 times as often.
+template <int N>
+__device__ __forceinline__ void load_q(const bf16 *q, int g, int G, uint32_t (&f)[N][2]) {
+    const int j = threadIdx.x & 3;
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) {
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (g < G) v = *reinterpret_cast<const uint4 *>(q + (int64_t)g * (N * 16) + (4 * i + j) * 8);
+        uint32_t x[4] = {v.x, v.y, v.z, v.w};  // words 0 .. 3 of chunk 4 i + j
+#pragma unroll
+        for (int d = 1; d < 4; d <<= 1)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (!(k & d)) {
+                    const uint32_t y = __shfl_xor_sync(0xffffffffu, j & d ? x[k] : x[k + d], d);
+                    if (j & d) x[k] = y; else x[k + d] = y;
+                }
+        f[2 * i][0] = x[0];  // now word j of chunks 4 i .. 4 i + 3
+        f[2 * i][1] = x[1];
+        f[2 * i + 1][0] = x[2];
+        f[2 * i + 1][1] = x[3];
+    }
+}
+
+// A place in a run: step `chunk` of the `n` steps of (sequence b, key head h).
 struct Place {
     int b, h, chunk, n, len;
     __device__ __forceinline__ void next(const AttnDecode &a) {
@@ -108,175 +135,185 @@ struct Place {
         h = 0;
         for (n = 0; n == 0 && ++b < a.B;) {
             len = length_of(a, b);
-            n = units_of(len);
+            n = steps_of(len);
         }
     }
 };
 
-// The CTA behind the last run checks lengths and page numbers and alone writes the error word.
-__device__ __forceinline__ void check_pages(const AttnDecode &a) {
-    bool bad = false;
-    const int page_size = 1 << a.page_log;
-    const int64_t most = (int64_t)a.max_pages << a.page_log;
-    for (int b = threadIdx.x >> 5; b < a.B; b += kWarps) {
-        const int len = a.lens[b];
-        bad |= len < 0 || len > most;
-        const int n = (int)min((int64_t)a.max_pages, ((int64_t)max(len, 0) + page_size - 1) >> a.page_log);
-        for (int i = threadIdx.x & 31; i < n; i += 32) {
-            const int p = a.table[(int64_t)b * a.max_pages + i];
-            bad |= p < 0 || p >= a.num_pages;
-        }
-    }
-    for (int i = threadIdx.x; i < (a.prefix_len + page_size - 1) >> a.page_log; i += kThreads)
-        bad |= a.prefix_pages[i] < 0 || a.prefix_pages[i] >= a.num_pages;
-    bad = __syncthreads_or(bad);
-    if (threadIdx.x == 0) {
-        if (a.prefix_len) {  // the prefix kernel cleared the word and may have set a bit
-            grid_wait();
-            if (bad) atomicOr(a.err, ERRBIT_PAGES);
-        } else {
-            *a.err = bad ? ERRBIT_PAGES : 0u;
-        }
-    }
-}
+// What the CTA's warps leave for the end: up to two pieces each.
+struct PieceTable {
+    int seg[2 * kWarps];   // b Hkv + h, or -1
+    int ends[2 * kWarps];  // whether it comes to that one's end
+};
 
 template <int D, int NT>
-__global__ void __launch_bounds__(kThreads, 1) k_attn_decode(const __grid_constant__ AttnDecode a) {
-    using S = Smem<D>;
+__global__ void __launch_bounds__(kThreads, 1)
+    k_attn_decode(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                  const __grid_constant__ AttnDecode a) {
+    using S = Smem<D, NT>;
     extern __shared__ __align__(1024) uint8_t smem[];
     grid_launch_dependents();
-    if (blockIdx.x == kDecodeCtas) {
-        check_pages(a);
-        return;
-    }
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t ring = tc::smem_u32(smem) + warp * S::RING;
-    float *mrg = reinterpret_cast<float *>(smem + S::OFF_MRG);
-    float2 *mrg_ml = reinterpret_cast<float2 *>(smem + S::OFF_ML);
+    float2 *const piece_ml = reinterpret_cast<float2 *>(smem + S::OFF_ML);  // [2 warp + (0 first, 1 last)][heads]
+    __shared__ int warp_sum[kWarps];
+    // steps of one key head before each thread's stretch of sequences, where pieces will be once all have read it
+    int *const stretch = reinterpret_cast<int *>(smem + S::OFF_FIRST);
+    int *const lens_of = reinterpret_cast<int *>(stretch + kThreads);  // and the lengths, with a sequence a thread
+    __shared__ PieceTable pieces;
+    __shared__ uint64_t bars[kWarps][S::NST];  // a stage has landed
+    __shared__ Ctl ctl;
+    bool bad = false, timed_out = false;  // a length or page number outside its range; a wait that gave up
+    if (lane == 0) {
+        for (int i = 0; i < S::NST; ++i) tc::mbar_init(&bars[warp][i], 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (tid == 0) ctl.abort = 0;
 
-    // ---- this CTA's run: a scan of the sequences' unit counts, a run of sequences per thread
-    __shared__ int64_t warp_sum[kWarps];
-    __shared__ int64_t found[3];  // sequence, units before it, total
+    if (ring & 1023u) {  // the boxes' swizzle counts on it
+        if (tid == 0) a.bad[blockIdx.x] = ERRBIT_INTERNAL;
+        if (a.prefix_len) grid_wait();
+        return;
+    }
+
+    // ---- the runs: a scan of the sequences' step counts, a stretch of sequences per thread
     const int per = (a.B + kThreads - 1) / kThreads;
-    int64_t mine = 0;
-    for (int b = tid * per; b < min(a.B, (tid + 1) * per); ++b) mine += units_of(length_of(a, b));
-    int64_t upto = mine;
+    int mine = 0;
+    for (int b = tid * per; b < min(a.B, (tid + 1) * per); ++b) {
+        const int len = length_of(a, b);
+        bad |= len != a.lens[b];
+        mine += steps_of(len);
+        if (per == 1) lens_of[tid] = len;
+    }
+    int upto = mine;
 #pragma unroll
     for (int m = 1; m < 32; m <<= 1) {
-        const int64_t x = __shfl_up_sync(0xffffffffu, upto, m);
+        const int x = __shfl_up_sync(0xffffffffu, upto, m);
         if (lane >= m) upto += x;
     }
     if (lane == 31) warp_sum[warp] = upto;
+    if (tid < 2 * kWarps) pieces.seg[tid] = -1;
     __syncthreads();
-    int64_t total = 0;
+    int total = 0;
+#pragma unroll
     for (int w = 0; w < kWarps; ++w) {
         if (w < warp) upto += warp_sum[w];
         total += warp_sum[w];
     }
-    const int64_t units = total * a.Hkv;
-    const int64_t u0 = first_unit(units, blockIdx.x), u1 = first_unit(units, blockIdx.x + 1);
-    if (u0 == u1) {
-        // nothing to read; sequences without keys are written by the combine kernel
-        if (a.prefix_len) grid_wait();
-        return;
-    }
-    if (u0 >= (upto - mine) * a.Hkv && u0 < upto * a.Hkv) {
-        int64_t before = upto - mine;
-        int b = tid * per;
-        for (;; ++b) {
-            const int n = units_of(length_of(a, b));
-            if (u0 < (before + n) * a.Hkv) break;
-            before += n;
+    const int steps = total * a.Hkv;
+    const int run0 = blockIdx.x * kWarps;
+    stretch[tid] = upto - mine;
+    __syncthreads();
+    const int u0 = first_step(steps, run0 + warp), u1 = first_step(steps, run0 + warp + 1);
+
+    Place at{};
+    if (u0 < u1) {
+        // the last stretch that starts at or before u0, and the sequence in it
+        int last = -1;
+#pragma unroll
+        for (int i = 0; i < kThreads / 32; ++i)
+            last += __popc(__ballot_sync(0xffffffffu, stretch[i * 32 + lane] * a.Hkv <= u0));
+        int in = u0 - stretch[last] * a.Hkv;
+        for (at.b = last * per;; ++at.b) {
+            at.len = per == 1 ? lens_of[at.b] : length_of(a, at.b);
+            at.n = steps_of(at.len);
+            if (in < at.n * a.Hkv) break;
+            in -= at.n * a.Hkv;
         }
-        found[0] = b;
-        found[1] = before;
+        at.h = (int)((uint32_t)in / (uint32_t)at.n);
+        at.chunk = in - at.h * at.n;
     }
     __syncthreads();
-    Place at;
-    at.b = (int)found[0];
-    at.len = length_of(a, at.b);
-    at.n = units_of(at.len);
-    {
-        const int64_t in = u0 - found[1] * a.Hkv;
-        at.h = (int)(in / at.n);
-        at.chunk = (int)(in - (int64_t)at.h * at.n);
-    }
 
-    // ---- loads: the page number is fetched one unit ahead of the copies
-    Place ld = at;
-    int64_t ld_u = u0;
-    auto page_of = [&](const Place &p) {
-        const int key = p.chunk * kUnit + warp * kStep;
-        return key < p.len ? a.table[(int64_t)p.b * a.max_pages + (key >> a.page_log)] : -1;
-    };
-    int page = page_of(ld);
-    int ld_st = 0;
-    auto load = [&]() {
-        if (ld_u < u1) {
-            const int key = ld.chunk * kUnit + warp * kStep, n = min(ld.len - key, kStep);
-            if (n > 0) {
+    if (u0 < u1) {
+        // ---- loads: a lane holds the page number of one of 32 consecutive steps of a sequence (any of its heads)
+        Place ld = at;
+        int ld_u = u0;
+        int ids = -1, ids_at = 0;  // of steps ids_at + lane
+        auto fetch_ids = [&]() {
+            ids_at = ld.chunk;
+            if (ld.chunk + lane < ld.n)
+                ids = a.table[(int64_t)ld.b * a.max_pages + ((int64_t)(ld.chunk + lane) * kStep >> a.page_log)];
+        };
+        fetch_ids();
+        int ld_st = 0;
+        auto load = [&]() {
+            if (ld_u < u1) {
+                const int page = __shfl_sync(0xffffffffu, ids, ld.chunk - ids_at);
                 const bool there = page >= 0 && page < a.num_pages;
-                const int64_t row = there ? ((((int64_t)page * a.Hkv + ld.h) << a.page_log) | (key & ((1 << a.page_log) - 1))) : 0;
-                const bf16 *k = a.k_cache + row * D, *v = a.v_cache + row * D;
-                const uint32_t dst = ring + ld_st * 2 * S::HALF;
-#pragma unroll
-                for (int i = 0; i < kStep * D / 8 / 32; ++i) {
-                    const int id = i * 32 + lane, r = id / (D / 8), c = id % (D / 8);
-                    const bool in = there && r < n;  // places past the end are filled with zeros
-                    const uint32_t off = r * (D * 2) + ((c ^ (r & 7)) << 4);
-                    const int64_t src = in ? r * D + c * 8 : 0;
-                    chunk::cp_async16(dst + off, k + src, in ? 16u : 0u);
-                    chunk::cp_async16(dst + S::HALF + off, v + src, in ? 16u : 0u);
+                bad |= !there;
+                uint64_t *bar = &bars[warp][ld_st];
+                if (lane == 0) tc::mbar_arrive_expect_tx(bar, 2 * S::HALF);
+                __syncwarp();
+                if (lane < 2 * (D / 64)) {  // K's and V's 64-column halves; a page that is none reads as zeros
+                    const int kv = lane / (D / 64), hf = lane % (D / 64);
+                    tc::tma_load_3d(ring + ld_st * 2 * S::HALF + kv * S::HALF + hf * (kStep * 128), kv ? &tm_v : &tm_k, bar, hf * 64,
+                                    ld.chunk * kStep & ((1 << a.page_log) - 1), (there ? page : a.num_pages) * a.Hkv + ld.h);
                 }
+                const int b = ld.b;
+                ld.next(a);
+                if (++ld_u < u1 && (ld.b != b || ld.chunk < ids_at || ld.chunk >= ids_at + 32)) fetch_ids();
             }
-            ld.next(a);
-            if (++ld_u < u1) page = page_of(ld);
-        }
-        chunk::cp_async_commit();
-        ld_st = ld_st + 1 == S::NST ? 0 : ld_st + 1;
-    };
-#pragma unroll
-    for (int i = 0; i < S::NST - 1; ++i) load();
+            ld_st = ld_st + 1 == S::NST ? 0 : ld_st + 1;
+        };
 
-    uint32_t qf[NT][D / 16][2];
-    float o[NT][D / 16][4], m[NT][2], l[NT][2];
-    const bool starts_before = at.chunk > 0;  // the first piece's head lies in an earlier CTA
-    bool fresh = true, first_piece = true;
-    int st = 0;
-    for (int64_t u = u0; u < u1; ++u) {
-        if (fresh) {
-            fresh = false;
+        uint32_t qf[NT][D / 16][2];
+        float o[NT][D / 16][4], m[NT][2], l[NT][2];
+        bool started_before = at.chunk > 0, fresh = true;
+        int st = 0, phase = 0;
+        for (int u = u0 - (S::NST - 1); u < u1; ++u) {
+            __syncwarp();
+            load();  // NST - 1 steps ahead, into the stage that was read one step ago
+            if (u < u0) continue;
+            if (fresh) {
+                fresh = false;
 #pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                const int g = t * 8 + (lane >> 2);
-                const bf16 *q = a.q + ((int64_t)at.b * a.Hq + at.h * a.G + min(g, a.G - 1)) * D + (lane & 3) * 2;
+                for (int t = 0; t < NT; ++t) {
+                    load_q(a.q + ((int64_t)at.b * a.Hq + at.h * a.G) * D, t * 8 + (lane >> 2), a.G, qf[t]);
 #pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk) {
-                    qf[t][kk][0] = g < a.G ? *reinterpret_cast<const uint32_t *>(q + kk * 16) : 0u;
-                    qf[t][kk][1] = g < a.G ? *reinterpret_cast<const uint32_t *>(q + kk * 16 + 8) : 0u;
-                    o[t][kk][0] = o[t][kk][1] = o[t][kk][2] = o[t][kk][3] = 0.f;
+                    for (int kk = 0; kk < D / 16; ++kk) o[t][kk][0] = o[t][kk][1] = o[t][kk][2] = o[t][kk][3] = 0.f;
+                    m[t][0] = m[t][1] = -INFINITY;
+                    l[t][0] = l[t][1] = 0.f;
                 }
-                m[t][0] = m[t][1] = -INFINITY;
-                l[t][0] = l[t][1] = 0.f;
             }
-        }
-        cp_async_wait<S::NST - 2>();
-        __syncwarp();
-        load();  // into the stage that was read one unit ago
-        const int n = min(at.len - at.chunk * kUnit - warp * kStep, kStep);
-        if (n > 0) {
+            if (!attn::wait_bar_w(&bars[warp][st], phase, &ctl, nullptr)) {
+                // gave up (or another warp did): its own copies still have to land before the CTA may end
+                timed_out = true;
+                for (int i = 1; i < S::NST; ++i) {
+                    st = st + 1 == S::NST ? 0 : st + 1;
+                    phase ^= st == 0;
+                    if (lane == 0 && u + i < ld_u) attn::drain_bar(&bars[warp][st], phase);
+                }
+                break;
+            }
+            const int n = at.len - at.chunk * kStep;  // keys of the step, at least 1; 16 or more: all
             const uint32_t kb = ring + st * 2 * S::HALF, vb = kb + S::HALF;
-            float s[NT][4];
+            if (n < kStep) {
+                // places past the end: whatever stale slots hold; K's scores are masked, V's rows become zeros
+                for (int i = n * (D / 8) + lane; i < kStep * (D / 8); i += 32) {
+                    const int r = i / (D / 8), c = i % (D / 8);
+                    chunk::st_shared_v4(vb + (c >> 3) * (kStep * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4), 0, 0, 0, 0);
+                }
+                tc::fence_smem_to_async();  // before TMA writes here again
+                __syncwarp();
+            }
+            float s[NT][4], s2[NT][4];  // two sums: a chain of half the length
 #pragma unroll
-            for (int t = 0; t < NT; ++t) s[t][0] = s[t][1] = s[t][2] = s[t][3] = 0.f;
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) s[t][i] = s2[t][i] = 0.f;
             const int kr = lane & 15, kc = lane >> 4;
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk) {
                 uint32_t f[4];
-                ldmatrix4(kb + kr * (D * 2) + (((2 * kk + kc) ^ (kr & 7)) << 4), f);
+                ldmatrix4(kb + (kk >> 2) * (kStep * 128) + kr * 128 + (((2 * (kk & 3) + kc) ^ (kr & 7)) << 4), f);
 #pragma unroll
-                for (int t = 0; t < NT; ++t) mma16816(s[t], f, qf[t][kk][0], qf[t][kk][1]);
+                for (int t = 0; t < NT; ++t) mma16816(kk & 1 ? s2[t] : s[t], f, qf[t][kk][0], qf[t][kk][1]);
             }
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) s[t][i] += s2[t][i];
             // this lane: keys lane / 4 and lane / 4 + 8, heads 2 (lane % 4) and one more
             const bool in0 = (lane >> 2) < n, in1 = (lane >> 2) + 8 < n;
             uint32_t pf[NT][2];
@@ -317,166 +354,281 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_decode(const __grid_consta
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk) {
                 uint32_t f[4];
-                ldmatrix4_t(vb + vr * (D * 2) + (((2 * kk + vc) ^ (vr & 7)) << 4), f);
+                ldmatrix4_t(vb + (kk >> 2) * (kStep * 128) + vr * 128 + (((2 * (kk & 3) + vc) ^ (vr & 7)) << 4), f);
 #pragma unroll
                 for (int t = 0; t < NT; ++t) mma16816(o[t][kk], f, pf[t][0], pf[t][1]);
             }
-        }
-        st = st + 1 == S::NST ? 0 : st + 1;
+            st = st + 1 == S::NST ? 0 : st + 1;
+            phase ^= st == 0;
 
-        const bool piece_ends = at.chunk + 1 == at.n || u + 1 == u1;
-        if (piece_ends) {
-            // ---- join the warps' pieces of this (sequence, head)
-            const bool whole = at.chunk + 1 == at.n && !(first_piece && starts_before);
+            const bool ends = at.chunk + 1 == at.n;
+            if (ends || u + 1 == u1) {
 #pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                const int heads = min(a.G - t * 8, 8);
-                if (heads <= 0) break;
+                for (int t = 0; t < NT; ++t)
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    float x = l[t][i];
-                    x += __shfl_xor_sync(0xffffffffu, x, 4);
-                    x += __shfl_xor_sync(0xffffffffu, x, 8);
-                    x += __shfl_xor_sync(0xffffffffu, x, 16);
-                    if (lane < 4) mrg_ml[warp * 8 + 2 * lane + i] = make_float2(m[t][i], x);
-                }
-                float *mine_o = mrg + (warp * 8 + (lane & 3) * 2) * S::LD + (lane >> 2);
-#pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) mine_o[(i & 1) * S::LD + kk * 16 + (i >> 1) * 8] = o[t][kk][i];
-                __syncthreads();
-                for (int e = tid; e < heads * (D / 4); e += kThreads) {
-                    const int g = e / (D / 4), d = e % (D / 4) * 4;
-                    float top = -INFINITY;
-#pragma unroll
-                    for (int w = 0; w < kWarps; ++w) top = fmaxf(top, mrg_ml[w * 8 + g].x);
-                    float sum = 0.f;
-                    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-                    for (int w = 0; w < kWarps; ++w) {
-                        const float2 ml = mrg_ml[w * 8 + g];
-                        const float f = ml.x == -INFINITY ? 0.f : exp2f(ml.x - top);
-                        const float4 y = *reinterpret_cast<const float4 *>(mrg + (w * 8 + g) * S::LD + d);
-                        sum += f * ml.y;
-                        x.x += f * y.x;
-                        x.y += f * y.y;
-                        x.z += f * y.z;
-                        x.w += f * y.w;
+                    for (int i = 0; i < 2; ++i) {
+                        float x = l[t][i];
+                        x += __shfl_xor_sync(0xffffffffu, x, 4);
+                        x += __shfl_xor_sync(0xffffffffu, x, 8);
+                        l[t][i] = x + __shfl_xor_sync(0xffffffffu, x, 16);
                     }
-                    const int head = t * 8 + g;
-                    if (whole && !a.prefix_len) {
-                        const float inv = 1.f / sum;
-                        *reinterpret_cast<uint2 *>(a.o + ((int64_t)at.b * a.Hq + at.h * a.G + head) * D + d) =
-                            make_uint2(tc::pack_bf16x2(x.x * inv, x.y * inv), tc::pack_bf16x2(x.z * inv, x.w * inv));
+                const int c = (lane & 3) * 2, r = lane >> 2;  // this lane: heads c, c + 1 (of 8), columns r, r + 8 (of 16)
+                if (ends && !started_before) {
+                    // the whole (sequence, head) in this run
+                    if (a.prefix_len) {
+                        const int64_t row = (2 * (int64_t)kDecodeCtas + (int64_t)at.b * a.Hkv + at.h) * a.G;
+#pragma unroll
+                        for (int t = 0; t < NT; ++t)
+#pragma unroll
+                            for (int i = 0; i < 2; ++i) {
+                                const int g = t * 8 + c + i;
+                                if (g >= a.G) continue;
+                                if (r == 0) a.slot_ml[row + g] = make_float2(m[t][i], l[t][i]);
+#pragma unroll
+                                for (int kk = 0; kk < D / 16; ++kk) {
+                                    a.slot_o[(row + g) * D + kk * 16 + r] = o[t][kk][i];
+                                    a.slot_o[(row + g) * D + kk * 16 + r + 8] = o[t][kk][i + 2];
+                                }
+                            }
                     } else {
-                        const int64_t row = (whole ? 2 * (int64_t)kDecodeCtas + (int64_t)at.b * a.Hkv + at.h
-                                                   : 2 * (int64_t)blockIdx.x + (first_piece && starts_before ? 0 : 1)) * a.G + head;
-                        *reinterpret_cast<float4 *>(a.slot_o + row * D + d) = x;
-                        if (d == 0) a.slot_ml[row] = make_float2(top, sum);
+#pragma unroll
+                        for (int t = 0; t < NT; ++t) {
+                            const float i0 = 1.f / l[t][0], i1 = 1.f / l[t][1];
+                            const int g = t * 8 + r;  // transposed: head r, columns c, c + 1 of 8
+                            bf16 *dst = a.o + ((int64_t)at.b * a.Hq + at.h * a.G + g) * D + c;
+#pragma unroll
+                            for (int kk = 0; kk < D / 16; ++kk) {
+                                const uint32_t lo = transpose8(tc::pack_bf16x2(o[t][kk][0] * i0, o[t][kk][1] * i1));
+                                const uint32_t hi = transpose8(tc::pack_bf16x2(o[t][kk][2] * i0, o[t][kk][3] * i1));
+                                if (g < a.G) {
+                                    *reinterpret_cast<uint32_t *>(dst + kk * 16) = lo;
+                                    *reinterpret_cast<uint32_t *>(dst + kk * 16 + 8) = hi;
+                                }
+                            }
+                        }
+                    }
+                } else {
+                    // a piece: the run's first, kept beside the ring, or its last, over the ring, which is done with
+                    const int which = started_before ? 0 : 1;
+                    __syncwarp();
+                    float *po = reinterpret_cast<float *>(smem + (which ? warp * S::RING : S::OFF_FIRST + warp * S::PIECE));
+#pragma unroll
+                    for (int t = 0; t < NT; ++t)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const int g = t * 8 + c + i;
+                            if (r == 0) piece_ml[(2 * warp + which) * NT * 8 + g] = make_float2(m[t][i], l[t][i]);
+#pragma unroll
+                            for (int kk = 0; kk < D / 16; ++kk) {
+                                po[g * S::LD + kk * 16 + r] = o[t][kk][i];
+                                po[g * S::LD + kk * 16 + r + 8] = o[t][kk][i + 2];
+                            }
+                        }
+                    if (lane == 0) {
+                        pieces.seg[2 * warp + which] = at.b * a.Hkv + at.h;
+                        pieces.ends[2 * warp + which] = ends;
                     }
                 }
-                __syncthreads();
+                fresh = true;
+                started_before = false;
             }
-            fresh = true;
-            first_piece = false;
+            at.next(a);
         }
-        at.next(a);
     }
-    cp_async_wait<0>();
+
+    // ---- join the warps' pieces: those of a (sequence, head) stand next to each other
+    const bool any = __syncthreads_or(bad || timed_out);
+    if (!any) {
+        if (tid == 0) a.bad[blockIdx.x] = 0u;
+    } else {
+        const bool pages = __syncthreads_or(bad), late = __syncthreads_or(timed_out);
+        if (tid == 0) a.bad[blockIdx.x] = (pages ? ERRBIT_PAGES : 0u) | (late ? ERRBIT_TIMEOUT : 0u);
+    }
+    static_assert(2 * kWarps <= 32, "");
+    const int my_seg = lane < 2 * kWarps ? pieces.seg[lane] : -1;
+    const uint32_t ending = __ballot_sync(0xffffffffu, lane < 2 * kWarps && pieces.ends[lane]);
+    const uint32_t same = __match_any_sync(0xffffffffu, my_seg);
+    uint32_t leaders = __ballot_sync(0xffffffffu, my_seg >= 0 && (same & ((1u << lane) - 1)) == 0);
+    for (int item = 0; leaders; leaders &= leaders - 1) {
+        const int first = __ffs(leaders) - 1;
+        const int seg = __shfl_sync(0xffffffffu, my_seg, first);
+        const uint32_t members = __shfl_sync(0xffffffffu, same, first);
+        // what the CTA's run starts in the middle of (its first piece) goes to slot 0, what it cuts off to slot 1
+        const bool before = first == 0, whole = !before && (ending >> (31 - __clz(members)) & 1);
+        const int b = seg / a.Hkv, h = seg - b * a.Hkv;
+        const int64_t row = (whole ? 2 * (int64_t)kDecodeCtas + seg : 2 * (int64_t)blockIdx.x + (before ? 0 : 1)) * a.G;
+        for (int g = 0; g < a.G; ++g, ++item) {  // a warp takes every eighth head
+            if ((item & (kWarps - 1)) != warp) continue;
+            float2 ml = make_float2(-INFINITY, 0.f);
+            if (members >> lane & 1) ml = piece_ml[lane * NT * 8 + g];
+            float top = ml.x;
+#pragma unroll
+            for (int i = 16; i; i >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, i));
+            const float f = ml.x == -INFINITY ? 0.f : exp2f(ml.x - top);
+            float sum = f * ml.y;
+#pragma unroll
+            for (int i = 16; i; i >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, i);
+            const int d = (lane & (D / 4 - 1)) * 4;
+            float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (uint32_t left = members; left; left &= left - 1) {
+                const int p = __ffs(left) - 1;
+                const float fp = __shfl_sync(0xffffffffu, f, p);
+                const float4 y = *reinterpret_cast<const float4 *>(
+                    smem + ((p & 1) ? (p >> 1) * S::RING : S::OFF_FIRST + (p >> 1) * S::PIECE) + (g * S::LD + d) * 4);
+                x.x += fp * y.x;
+                x.y += fp * y.y;
+                x.z += fp * y.z;
+                x.w += fp * y.w;
+            }
+            if (lane >= D / 4) continue;
+            if (whole && !a.prefix_len) {
+                const float inv = 1.f / sum;
+                *reinterpret_cast<uint2 *>(a.o + ((int64_t)b * a.Hq + h * a.G + g) * D + d) =
+                    make_uint2(tc::pack_bf16x2(x.x * inv, x.y * inv), tc::pack_bf16x2(x.z * inv, x.w * inv));
+            } else {
+                *reinterpret_cast<float4 *>(a.slot_o + (row + g) * D + d) = x;
+                if (d == 0) a.slot_ml[row + g] = make_float2(top, sum);
+            }
+        }
+    }
     if (a.prefix_len) grid_wait();  // this kernel's end then means the prefix kernel's too
 }
 
 // One CTA per (sequence, query head): joins the pieces of its own keys with those of the prefix. A row
 // that the decode kernel finished is left alone; one without any keys is zero.
+constexpr int kMostPieces = 2 * kDecodeCtas;  // a piece per CTA and per split of the prefix at most
 template <int D>
 __global__ void __launch_bounds__(128) k_attn_combine(const __grid_constant__ AttnDecode a) {
-    constexpr int LPR = D / 4, SUBS = 128 / LPR;  // lanes per row; pieces in flight
+    constexpr int LPR = D / 4, SUBS = 128 / LPR, AHEAD = 4;  // lanes per row; pieces read together; and ahead
     const int row = blockIdx.x, b = row / a.Hq, hq = row - b * a.Hq, h = hq / a.G, g = hq - h * a.G;
     const int tid = threadIdx.x, sub = tid / LPR, d = tid % LPR * 4;
-    __shared__ int64_t sums[2];
+    __shared__ int sums[2][4];
+    __shared__ float weight[kMostPieces], red[2][4];
     __shared__ float4 part[SUBS][LPR];
-    __shared__ float2 part_ml[SUBS];
-    if (tid < 2) sums[tid] = 0;
-    __syncthreads();
-    int64_t before = 0, total = 0;
+    int before = 0, total = 0;
     for (int i = tid; i < a.B; i += 128) {
-        const int n = units_of(length_of(a, i));
+        const int n = steps_of(length_of(a, i));
         total += n;
         if (i < b) before += n;
     }
-#pragma unroll
-    for (int m = 16; m; m >>= 1) {
-        before += __shfl_xor_sync(0xffffffffu, before, m);
-        total += __shfl_xor_sync(0xffffffffu, total, m);
-    }
+    const int n = steps_of(length_of(a, b));
+    before = __reduce_add_sync(0xffffffffu, before);
+    total = __reduce_add_sync(0xffffffffu, total);
     if ((tid & 31) == 0) {
-        atomicAdd(reinterpret_cast<unsigned long long *>(&sums[0]), (unsigned long long)before);
-        atomicAdd(reinterpret_cast<unsigned long long *>(&sums[1]), (unsigned long long)total);
+        sums[0][tid >> 5] = before;
+        sums[1][tid >> 5] = total;
+    }
+    bool bad = false;
+    if (row == 0) {
+        const int np = (int)(((int64_t)a.prefix_len + (1 << a.page_log) - 1) >> a.page_log);
+        for (int i = tid; i < np; i += 128) bad |= a.prefix_pages[i] < 0 || a.prefix_pages[i] >= a.num_pages;
     }
     __syncthreads();
-    const int64_t units = sums[1] * a.Hkv;
-    const int n = units_of(length_of(a, b));
-    const int64_t x0 = sums[0] * a.Hkv + (int64_t)h * n;
+    const int steps = (sums[1][0] + sums[1][1] + sums[1][2] + sums[1][3]) * a.Hkv;
+    const int x0 = (sums[0][0] + sums[0][1] + sums[0][2] + sums[0][3]) * a.Hkv + h * n;
     int c0 = 0, own = 0;  // first CTA with a piece, number of pieces
     if (n) {
-        c0 = cta_of(units, x0);
-        own = cta_of(units, x0 + n - 1) - c0 + 1;
+        c0 = cta_of(steps, x0);
+        own = cta_of(steps, x0 + n - 1) - c0 + 1;
     }
+    const int all = own + (a.prefix_len ? a.splits : 0);
+    // piece i: a row of the slots, or of the prefix kernel's results
+    auto place = [&](int i, const float *&po, const float2 *&ml) {
+        const bool mine = i < own;
+        const int64_t r = !mine ? (int64_t)(i - own) * a.B * a.Hq + row
+                                : (own == 1 ? 2 * (int64_t)kDecodeCtas + (int64_t)b * a.Hkv + h
+                                            : 2 * (int64_t)(c0 + i) + (i == 0 ? 1 : 0)) * a.G + g;
+        po = (mine ? a.slot_o : a.part_o) + r * D + d;
+        ml = (mine ? a.slot_ml : a.part_ml) + r;
+    };
+
     grid_wait();  // also where nothing is left to do: this kernel's end means the one before it has ended
+    if (row == 0) {
+        // the error word, from what the decode kernel's CTAs found (the prefix kernel has set it up already)
+        uint32_t found = bad ? ERRBIT_PAGES : 0u;
+        for (int i = tid; i < kDecodeCtas; i += 128) found |= a.bad[i];
+        const bool pages = __syncthreads_or(found & ERRBIT_PAGES), late = __syncthreads_or(found & ERRBIT_TIMEOUT),
+                   internal = __syncthreads_or(found & ERRBIT_INTERNAL);
+        if (tid == 0)
+            *a.err = (a.prefix_len ? *a.err : 0u) | (pages ? ERRBIT_PAGES : 0u) | (late ? ERRBIT_TIMEOUT : 0u) |
+                     (internal ? ERRBIT_INTERNAL : 0u);
+    }
     if (own == 1 && !a.prefix_len) return;
-    const int splits = a.prefix_len ? a.splits : 0;
-    float top = -INFINITY, sum = 0.f;
-    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int i = sub; i < own + splits; i += SUBS) {
-        const float *po;
-        float2 ml;
-        if (i < own) {
-            const int64_t slot = (own == 1 ? 2 * (int64_t)kDecodeCtas + (int64_t)b * a.Hkv + h
-                                           : 2 * (int64_t)(c0 + i) + (i == 0 ? 1 : 0)) * a.G + g;
-            po = a.slot_o + slot * D;
-            ml = a.slot_ml[slot];
-        } else {
-            const int64_t r = (int64_t)(i - own) * a.B * a.Hq + row;
-            po = a.part_o + r * D;
-            ml = a.part_ml[r];
+
+    // the first pieces set out while the weights are worked out
+    float4 y[AHEAD];
+    const float *po;
+    const float2 *pml;
+    auto fetch = [&](int i0) {
+#pragma unroll
+        for (int k = 0; k < AHEAD; ++k) {
+            const int i = i0 + k * SUBS;
+            y[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (i < all) {
+                place(i, po, pml);
+                y[k] = *reinterpret_cast<const float4 *>(po);
+            }
         }
-        const float4 y = *reinterpret_cast<const float4 *>(po + d);
-        const float t = fmaxf(top, ml.x);
-        const float fo = top == -INFINITY ? 0.f : exp2f(top - t), fn = ml.x == -INFINITY ? 0.f : exp2f(ml.x - t);
-        x.x = x.x * fo + y.x * fn;
-        x.y = x.y * fo + y.y * fn;
-        x.z = x.z * fo + y.z * fn;
-        x.w = x.w * fo + y.w * fn;
-        sum = sum * fo + ml.y * fn;
-        top = t;
+    };
+    fetch(sub);
+    float2 ml[(kMostPieces + 127) / 128];
+    float top = -INFINITY;
+#pragma unroll
+    for (int k = 0; k < (kMostPieces + 127) / 128; ++k) {
+        ml[k] = make_float2(-INFINITY, 0.f);
+        if (k * 128 + tid < all) {
+            place(k * 128 + tid, po, pml);
+            ml[k] = *pml;
+        }
+        top = fmaxf(top, ml[k].x);
+    }
+#pragma unroll
+    for (int i = 16; i; i >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, i));
+    if ((tid & 31) == 0) red[0][tid >> 5] = top;
+    __syncthreads();
+    top = fmaxf(fmaxf(red[0][0], red[0][1]), fmaxf(red[0][2], red[0][3]));
+    float sum = 0.f;
+#pragma unroll
+    for (int k = 0; k < (kMostPieces + 127) / 128; ++k) {
+        const float f = ml[k].x == -INFINITY ? 0.f : exp2f(ml[k].x - top);
+        if (k * 128 + tid < all) weight[k * 128 + tid] = f;
+        sum += f * ml[k].y;
+    }
+#pragma unroll
+    for (int i = 16; i; i >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, i);
+    if ((tid & 31) == 0) red[1][tid >> 5] = sum;
+    __syncthreads();
+    sum = (red[1][0] + red[1][1]) + (red[1][2] + red[1][3]);
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i0 = sub; i0 < all; i0 += AHEAD * SUBS) {
+#pragma unroll
+        for (int k = 0; k < AHEAD; ++k) {
+            const float f = i0 + k * SUBS < all ? weight[i0 + k * SUBS] : 0.f;
+            x.x += f * y[k].x;
+            x.y += f * y[k].y;
+            x.z += f * y[k].z;
+            x.w += f * y[k].w;
+        }
+        if (i0 + AHEAD * SUBS < all) fetch(i0 + AHEAD * SUBS);
     }
     part[sub][tid % LPR] = x;
-    if (d == 0) part_ml[sub] = make_float2(top, sum);
     __syncthreads();
     if (sub) return;
-    for (int i = 0; i < SUBS; ++i) top = fmaxf(top, part_ml[i].x);
-    sum = 0.f;
-    x = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-    for (int i = 0; i < SUBS; ++i) {
-        const float2 ml = part_ml[i];
-        const float f = ml.x == -INFINITY ? 0.f : exp2f(ml.x - top);
-        const float4 y = part[i][tid % LPR];
-        x.x += f * y.x;
-        x.y += f * y.y;
-        x.z += f * y.z;
-        x.w += f * y.w;
-        sum += f * ml.y;
+    for (int i = 1; i < SUBS; ++i) {
+        const float4 z = part[i][tid % LPR];
+        x.x += z.x;
+        x.y += z.y;
+        x.z += z.z;
+        x.w += z.w;
     }
-    const float inv = own + splits ? 1.f / sum : 0.f;
+    const float inv = all ? 1.f / sum : 0.f;
     *reinterpret_cast<uint2 *>(a.o + (int64_t)row * D + d) =
         make_uint2(tc::pack_bf16x2(x.x * inv, x.y * inv), tc::pack_bf16x2(x.z * inv, x.w * inv));
 }
 
-template <typename K>
-cudaError_t launch_pdl(K kern, unsigned grid, unsigned threads, size_t smem, cudaStream_t st, bool early, const AttnDecode &a) {
+template <typename K, typename... A>
+cudaError_t launch_pdl(K kern, unsigned grid, unsigned threads, size_t smem, cudaStream_t st, bool early, const A &...args) {
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(grid);
     cfg.blockDim = dim3(threads);
@@ -487,17 +639,23 @@ cudaError_t launch_pdl(K kern, unsigned grid, unsigned threads, size_t smem, cud
     at.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &at;
     cfg.numAttrs = early ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, kern, a);
+    return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
 template <int D, int NT>
 cudaError_t launch(AttnDecode a, cudaStream_t st, const char **stage) {
     cudaError_t e;
+    CUtensorMap tm_k, tm_v;
+    *stage = "TMA descriptor encoding";
+    const uint64_t page = 1u << a.page_log, n = (uint64_t)a.num_pages * a.Hkv;
+    if ((e = attn::make_map(&tm_k, a.k_cache, D, page, n, D, page * D, kStep, 1)) != cudaSuccess) return e;
+    if ((e = attn::make_map(&tm_v, a.v_cache, D, page, n, D, page * D, kStep, 1)) != cudaSuccess) return e;
     *stage = "attn_decode";
     auto kern = k_attn_decode<D, NT>;
-    if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Smem<D>::TOTAL)) != cudaSuccess) return e;
+    constexpr size_t smem = Smem<D, NT>::TOTAL;
+    if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) != cudaSuccess) return e;
     void *pr = prof_start("attn_decode", st);
-    e = launch_pdl(kern, kDecodeCtas + 1, kThreads, Smem<D>::TOTAL, st, a.prefix_len > 0, a);
+    e = launch_pdl(kern, kDecodeCtas, kThreads, smem, st, a.prefix_len > 0, tm_k, tm_v, a);
     prof_stop(pr);
     if (e != cudaSuccess) return e;
     *stage = "attn_combine";

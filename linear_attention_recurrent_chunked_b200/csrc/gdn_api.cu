@@ -519,12 +519,13 @@ gdn_status gdn_attn_prefill(const void *q, int64_t q_stride, const void *k, int6
 
 // Regions of gdn_attn_decode's workspace, each 256-byte aligned.
 struct DecodeWs {
-    size_t slot_o, slot_ml, part_o, part_ml, total;
+    size_t bad, slot_o, slot_ml, part_o, part_ml, total;
     DecodeWs(int B, int Hq, int Hkv, int d, int prefix_len) {
         const size_t slots = gdn::attn_decode_slots(B, Hq, Hkv, prefix_len);
         const size_t parts = (size_t)gdn::attn_decode_splits(B, Hq, Hkv, prefix_len) * B * Hq;
         auto up = [](size_t n) { return (n + 255) / 256 * 256; };
-        slot_o = kErrWordBytes;
+        bad = kErrWordBytes;
+        slot_o = bad + up(gdn::kDecodeCtas * sizeof(uint32_t));
         slot_ml = slot_o + up(slots * d * sizeof(float));
         part_o = slot_ml + up(slots * sizeof(float2));
         part_ml = part_o + up(parts * d * sizeof(float));
@@ -554,6 +555,8 @@ gdn_status gdn_attn_decode(const void *q, const void *k_cache, const void *v_cac
                     "slots)", num_pages, page_size);
     if (max_pages < 1 || (int64_t)max_pages * page_size > 1 << 30)
         return fail(GDN_ERR_SHAPE, "max_pages=%d out of range (at least 1, at most 2^30 keys a sequence)", max_pages);
+    if ((double)B * Hkv * max_pages * page_size >= 16.0 * INT32_MAX - 16.0 * B * Hkv)
+        return fail(GDN_ERR_SHAPE, "B=%d Hkv=%d max_pages=%d: more than 2^31 steps of 16 keys", B, Hkv, max_pages);
     if (!q || !k_cache || !v_cache || !page_table || !lens || !o || (prefix_len > 0 && !prefix_pages))
         return fail(GDN_ERR_NULL, "q, k_cache, v_cache, page_table, lens, o and (with prefix_len) prefix_pages are required");
     const void *ptrs[] = {q, k_cache, v_cache, o};
@@ -592,6 +595,7 @@ gdn_status gdn_attn_decode(const void *q, const void *k_cache, const void *v_cac
     a.slot_ml = reinterpret_cast<float2 *>(ws + w.slot_ml);
     a.part_o = reinterpret_cast<float *>(ws + w.part_o);
     a.part_ml = reinterpret_cast<float2 *>(ws + w.part_ml);
+    a.bad = reinterpret_cast<uint32_t *>(ws + w.bad);
     const char *stage = "";
     const cudaError_t e = gdn::launch_attn_decode(a, d, static_cast<cudaStream_t>(stream), &stage);
     if (e != cudaSuccess) return cuda_fail(e, stage);

@@ -87,7 +87,7 @@ DECODE = dict(q=FAKE, kc=FAKE, vc=FAKE, pages=64, page=16, table=FAKE, max_pages
     (dict(dt=0), 3), (dict(d=96), 2), (dict(B=0), 2), (dict(Hq=0), 2), (dict(Hkv=0), 2), (dict(Hkv=3), 2), (dict(Hkv=0x7fffffff), 2),
     (dict(Hq=68), 2), (dict(prefix_len=-1), 2), (dict(prefix_len=(1 << 30) + 1), 2), (dict(B=1 << 29), 2),
     (dict(page=8), 2), (dict(page=48), 2), (dict(page=256), 2), (dict(pages=0), 2), (dict(pages=1 << 27), 2),
-    (dict(max_pages=0), 2), (dict(max_pages=(1 << 26) + 1), 2), (dict(pages=1 << 26, Hkv=32, Hq=32), 2),
+    (dict(max_pages=0), 2), (dict(max_pages=(1 << 26) + 1), 2), (dict(max_pages=1 << 26, B=1 << 10), 2), (dict(pages=1 << 26, Hkv=32, Hq=32), 2),
     (dict(q=None), 1), (dict(kc=None), 1), (dict(vc=None), 1), (dict(table=None), 1), (dict(lens=None), 1), (dict(o=None), 1),
     (dict(prefix_pages=None), 1), (dict(q=MIS), 4), (dict(kc=MIS), 4), (dict(o=MIS), 4), (dict(table=ODD), 4), (dict(lens=ODD), 4),
     (dict(prefix_pages=ODD), 4), (dict(ws=None), 6), (dict(ws_bytes=256), 6), (dict(ws=VP((1 << 20) + 16)), 4),
