@@ -103,6 +103,14 @@ __device__ __forceinline__ void exp2_poly(uint64_t x, float &r0, float &r1) {
     r1 = __uint_as_float((__float_as_uint(t1) << 23) + __float_as_uint(p1));
 }
 
+// Eight fp32 values to a 32-byte aligned place: a whole sector from one thread.
+__device__ __forceinline__ void st_global8(float *p, const float *x) {
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(__float_as_uint(x[0])),
+                 "r"(__float_as_uint(x[1])), "r"(__float_as_uint(x[2])), "r"(__float_as_uint(x[3])), "r"(__float_as_uint(x[4])),
+                 "r"(__float_as_uint(x[5])), "r"(__float_as_uint(x[6])), "r"(__float_as_uint(x[7]))
+                 : "memory");
+}
+
 // TMEM -> registers, 32 columns, without the wait (see tc::tmem_wait_ld).
 __device__ __forceinline__ void tmem_ld32x(uint32_t taddr, uint32_t (&u)[32]) {
     asm volatile(

@@ -669,10 +669,10 @@ cudaError_t launch(AttnDecode a, cudaStream_t st, const char **stage) {
 
 int attn_decode_splits(int B, int Hq, int Hkv, int prefix_len) {
     if (prefix_len <= 0) return 0;
-    // as many splits of the prefix's key tiles as fill the SMs once
+    // as many splits of the prefix's steps of 64 keys as fill the SMs once
     const int64_t pos = 2 * (128 / (Hq / Hkv)), blocks = (B + pos - 1) / pos * Hkv;
-    const int64_t tiles = ((int64_t)prefix_len + 127) / 128;
-    return (int)std::max<int64_t>(1, std::min<int64_t>(tiles, kDecodeCtas / blocks));
+    const int64_t steps = ((int64_t)prefix_len + 63) / 64;
+    return (int)std::max<int64_t>(1, std::min<int64_t>(steps, kDecodeCtas / blocks));
 }
 
 size_t attn_decode_slots(int B, int Hq, int Hkv, int prefix_len) {

@@ -60,14 +60,15 @@ struct Layout {
     static constexpr uint32_t TILE = 128 * D * 2;      // D / 64 column blocks of 128 rows x 128 bytes
     static constexpr int NST = D == 128 ? 5 : 8;       // K and V tiles in the ring
     static constexpr uint32_t OFF_Q = 0, OFF_KV = 2 * TILE, OFF_BAR = OFF_KV + NST * TILE;
-    // barriers: Q landed, ring full / empty, per query tile: S complete, S read; per query tile and P buffer
-    // (2 u + buffer): P written, O += P V done; the first weights of tile 0; all products done
+    // barriers: Q landed, ring full / empty, per query tile: S complete, S read, P written, O += P V done, Q in
+    // tensor memory; the first weights of tile 0; all products done
     static constexpr int QFULL = 0, FULL = 1, EMPTY = FULL + NST, SFULL = EMPTY + NST, SFREE = SFULL + 2,
-                         PREADY = SFREE + 2, PVD = PREADY + 4, START = PVD + 4, FIN = START + 1, NBAR = FIN + 1;
+                         PREADY = SFREE + 2, QT = PREADY + 2, START = QT + 2, PVD = START + 1, FIN = PVD + 2, NBAR = FIN + 1;
     static constexpr uint32_t OFF_CTL = OFF_BAR + 8 * NBAR;
     static constexpr uint32_t SMEM = OFF_CTL + 16 + 1024;
-    // tensor memory columns: S of tile u at u * 64, P of tile u, buffer b at 128 + (2 u + b) * 32, O at 256 + u * D
-    static constexpr uint32_t TM_S = 0, TM_P = 128, TM_O = 256;
+    // tensor memory columns: S of tile u at u * 64, P at 128 + u * 32, Q of the first QT_TILES tiles, O at 256 + u * D
+    static constexpr uint32_t TM_S = 0, TM_P = 128, TM_Q = 192, TM_O = 256;
+    static constexpr int QT_TILES = 128 / D;
     static constexpr int POLY = D == 64 ? 2 : 0;       // of every 8 weights, those that the FMA pipe computes: see the softmax
 };
 
@@ -109,7 +110,8 @@ __device__ __forceinline__ void s_loop(std::integral_constant<int, U> u, int myn
     const uint32_t id_s = tc::make_idesc_bf16(TQ, STEP, 0, 0);  // both operands K-major
     const tc::Desc dq = tc::split_desc(tc::make_desc_sw128(sb + L::OFF_Q + u * L::TILE, 16, 1024));
     const tc::Desc dk = tc::split_desc(tc::make_desc_sw128(sb + L::OFF_KV, 16, 1024));
-    bool ok = wait_bar_w(&bar[L::QFULL], 0, ctl, err);
+    constexpr bool TS = U < L::QT_TILES;
+    bool ok = myns == 0 || wait_bar_w(&bar[TS ? L::QT + U : L::QFULL], 0, ctl, err);
     if (ok && U == 1 && myns > 0) ok = wait_bar_w(&bar[L::START], 0, ctl, err);
     for (int j = 0; ok && j < myns; ++j) {
         const int c = j & ~1;
@@ -121,7 +123,10 @@ __device__ __forceinline__ void s_loop(std::integral_constant<int, U> u, int myn
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
             const uint32_t off = (kk >> 2) * 16384 + (kk & 3) * 32;
-            tc::mma_bf16_off_w(tm + L::TM_S + u * 64, dq, off, dk, kb + off, id_s, kk > 0);
+            if (TS)
+                tc::mma_bf16_ts_off_w(tm + L::TM_S + u * 64, tm + L::TM_Q + u * (D / 2) + 8 * kk, dk, kb + off, id_s, kk > 0);
+            else
+                tc::mma_bf16_off_w(tm + L::TM_S + u * 64, dq, off, dk, kb + off, id_s, kk > 0);
         }
         tc::mma_commit_w(&bar[L::SFULL + u]);
         if ((j & 1) || j + 1 == myns) tc::mma_commit_w(&bar[L::EMPTY + c % L::NST]);
@@ -139,15 +144,15 @@ __device__ __forceinline__ void pv_loop(std::integral_constant<int, U> u, int my
     for (int j = 0; ok && j < myns; ++j) {
         const int b = j & 1, c = j | 1;
         if (!(ok = (b || ring_full<D>(bar, c, ctl, err)) &&
-                   wait_bar_w(&bar[L::PREADY + 2 * u + b], (uint32_t)((j >> 1) & 1), ctl, err)))
+                   wait_bar_w(&bar[L::PREADY + u], (uint32_t)(j & 1), ctl, err)))
             break;
         tc::fence_after_sync();
         const uint32_t vb = (uint32_t)(c % L::NST) * L::TILE + b * (STEP * 128);
 #pragma unroll
         for (int kk = 0; kk < STEP / 16; ++kk)
-            tc::mma_bf16_ts_off_w(tm + L::TM_O + u * D, tm + L::TM_P + (2 * u + b) * 32 + 8 * kk, dv, vb + kk * 2048, id_o,
+            tc::mma_bf16_ts_off_w(tm + L::TM_O + u * D, tm + L::TM_P + u * 32 + 8 * kk, dv, vb + kk * 2048, id_o,
                                   (j > 0 || kk > 0) ? 1u : 0u);
-        tc::mma_commit_w(&bar[L::PVD + 2 * u + b]);
+        tc::mma_commit_w(&bar[L::PVD + u]);
         if (b || j + 1 == myns) tc::mma_commit_w(&bar[L::EMPTY + c % L::NST]);
     }
 }
@@ -176,12 +181,12 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         it.t0 = 0;
         it.len = a.T_tot;
         it.pos0 = rb * 2 * P;
-        // key tiles spread over the splits as evenly as they go
-        const int tiles = (a.prefix_len + TK - 1) / TK;
-        const int k0 = (int)((int64_t)tiles * it.split / a.splits), k1 = (int)((int64_t)tiles * (it.split + 1) / a.splits);
-        it.k0 = k0 * TK;
+        // steps spread over the splits as evenly as they go
+        const int steps = (a.prefix_len + STEP - 1) / STEP;
+        const int k0 = (int)((int64_t)steps * it.split / a.splits), k1 = (int)((int64_t)steps * (it.split + 1) / a.splits);
+        it.k0 = k0 * STEP;
         it.keys = a.prefix_len - it.k0;
-        it.ns0 = (min(it.keys, (k1 - k0) * TK) + STEP - 1) / STEP;
+        it.ns0 = k1 - k0;
         it.ns1 = it.pos0 + P < it.len ? it.ns0 : 0;
     } else {
         // blocks are numbered so that the query tiles with the most key tiles come first
@@ -213,7 +218,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     Ctl *ctl = reinterpret_cast<Ctl *>(smem + L::OFF_CTL);
     if (warp == W_MMA) tc::tmem_alloc(&ctl->tmem, 512);
     if (tid == W_LOAD * 32) {
-        for (int i = 0; i < L::NBAR; ++i) tc::mbar_init(&bar[i], ((i >= L::SFREE && i < L::PVD) || i == L::START) ? 4u : i == L::FIN ? 4u : (i >= L::EMPTY && i < L::SFULL) ? 2u : 1u);
+        for (int i = 0; i < L::NBAR; ++i) tc::mbar_init(&bar[i], (i >= L::SFREE && i < L::PVD) ? 4u : i == L::FIN ? 4u : (i >= L::EMPTY && i < L::SFULL) ? 2u : 1u);
         ctl->abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -233,11 +238,12 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                                     it.t0 + it.pos0 + u * P);
         }
         __syncwarp();
-        // paged: lane i brings box i of a tile, whose page number it fetched a tile ahead
-        const int boxes = PREFIX ? TK >> a.page_log : 1, rows = TK / boxes;
+        // paged: lane i brings box i of a tile (a page's rows, 64 of them at most), whose page number it fetched a
+        // tile ahead
+        const int box_log = min(a.page_log, 6), boxes = PREFIX ? TK >> box_log : 1, rows = TK / boxes;
         const int npages = PREFIX ? (a.prefix_len + (1 << a.page_log) - 1) >> a.page_log : 0;
         auto page_of = [&](int j) {
-            const int i = ((it.k0 + j * TK) >> a.page_log) + lane;
+            const int i = (it.k0 + j * TK + (lane << box_log)) >> a.page_log;
             int p = a.num_pages;  // beyond the tensor: reads as zero
             if (lane < boxes && i < npages) {
                 const int x = a.pages[i];
@@ -264,7 +270,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
 #pragma unroll
                     for (int hf = 0; hf < D / 64; ++hf) {
                         if (PREFIX)
-                            tc::tma_load_3d(dst + hf * 16384, map, &bar[L::FULL + st], 64 * hf, 0, page * a.Hkv + it.head);
+                            tc::tma_load_3d(dst + hf * 16384, map, &bar[L::FULL + st], 64 * hf,
+                                            (it.k0 + j * TK + (lane << box_log)) & ((1 << a.page_log) - 1), page * a.Hkv + it.head);
                         else
                             tc::tma_load_3d(dst + hf * 16384, map, &bar[L::FULL + st], 64 * hf, it.head, it.k0 + j * TK);
                     }
@@ -301,8 +308,30 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         const float sc = a.scale_log2;
         float m_ref = -INFINITY, l = 0.f;
         bool ok = true;
+        if (u < L::QT_TILES && myns) {
+            // this row of Q to tensor memory, where the products for S read it without shared memory
+            ok = wait_bar_w(&bar[L::QFULL], 0, ctl, a.err);
+            if (ok) {
+#pragma unroll
+                for (int hf = 0; hf < D / 64; ++hf) {
+                    uint32_t w[32];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const uint4 x = *reinterpret_cast<const uint4 *>(smem + L::OFF_Q + u * L::TILE + hf * 16384 + r * 128 + ((i ^ (r & 7)) << 4));
+                        w[4 * i] = x.x;
+                        w[4 * i + 1] = x.y;
+                        w[4 * i + 2] = x.z;
+                        w[4 * i + 3] = x.w;
+                    }
+                    tc::tmem_st32(tl + L::TM_Q + u * (D / 2) + hf * 32, w);
+                }
+                tc::tmem_st_wait();
+                tc::fence_before_sync();
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(&bar[L::QT + u]);
+            }
+        }
         for (int j = 0; ok && j < myns; ++j) {
-            const int pbuf = 2 * u + (j & 1);
             const uint32_t ts = tl + L::TM_S + u * 64;
             if (!(ok = wait_bar_w(&bar[L::SFULL + u], (uint32_t)(j & 1), ctl, a.err))) break;
             tc::fence_after_sync();
@@ -338,8 +367,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                 l *= alpha;
             }
             if (j > 0 && __any_sync(0xffffffffu, grow)) {
-                const int pb = (j - 1) & 1;
-                if (!(ok = wait_bar_w(&bar[L::PVD + 2 * u + pb], (uint32_t)(((j - 1) >> 1) & 1), ctl, a.err))) break;
+                if (!(ok = wait_bar_w(&bar[L::PVD + u], (uint32_t)((j - 1) & 1), ctl, a.err))) break;
                 tc::fence_after_sync();
 #pragma unroll 1
                 for (int c0 = 0; c0 < D; c0 += 32) {
@@ -370,11 +398,11 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                 ps[i & 1] = attn::add2(ps[i & 1], attn::pack2(p0, p1));
                 w[i] = tc::pack_bf16x2(p0, p1);
             }
-            if (j >= 2) {  // P's buffer: read two steps ago
-                if (!(ok = wait_bar_w(&bar[L::PVD + pbuf], (uint32_t)(((j >> 1) & 1) ^ 1), ctl, a.err))) break;
+            if (j >= 1) {  // the last weights have been read
+                if (!(ok = wait_bar_w(&bar[L::PVD + u], (uint32_t)((j - 1) & 1), ctl, a.err))) break;
                 tc::fence_after_sync();
             }
-            tc::tmem_st32(tl + L::TM_P + pbuf * 32, w);
+            tc::tmem_st32(tl + L::TM_P + u * 32, w);
             float a0, a1;
             attn::unpack2(attn::add2(ps[0], ps[1]), a0, a1);
             l += a0 + a1;
@@ -396,12 +424,12 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             tc::fence_before_sync();
             __syncwarp();
             if (lane == 0) {
-                tc::mbar_arrive(&bar[L::PREADY + pbuf]);
+                tc::mbar_arrive(&bar[L::PREADY + u]);
                 if (u == 0 && j == 0) tc::mbar_arrive(&bar[L::START]);  // (PREADY's phases come round; this one's does not)
             }
         }
         if (ok && myns)
-            ok = wait_bar_w(&bar[L::PVD + 2 * u + ((myns - 1) & 1)], (uint32_t)(((myns - 1) >> 1) & 1), ctl, a.err);
+            ok = wait_bar_w(&bar[L::PVD + u], (uint32_t)((myns - 1) & 1), ctl, a.err);
         if (ok && myns) {
             tc::fence_after_sync();
             const bool valid = r < a.G * P && pos < it.len;
@@ -416,9 +444,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                     tc::tmem_ld32(to + c0, x);
                     if (valid) {
 #pragma unroll
-                        for (int i = 0; i < 32; i += 4)
-                            *reinterpret_cast<float4 *>(a.part_o + prow * D + c0 + i) =
-                                make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
+                        for (int i = 0; i < 32; i += 8) attn::st_global8(a.part_o + prow * D + c0 + i, x + i);
                     }
                 }
             } else {
@@ -473,8 +499,8 @@ cudaError_t launch_prefix(AttnPrefill a, cudaStream_t st, const char **stage) {
     *stage = "TMA descriptor encoding";
     const uint64_t page = 1u << a.page_log, n = (uint64_t)a.num_pages * a.Hkv;
     if ((e = attn::make_map(&tm_q, a.q, D, a.Hq, a.T_tot, D, (uint64_t)a.Hq * D, a.G, a.P)) != cudaSuccess) return e;
-    if ((e = attn::make_map(&tm_k, a.k, D, page, n, D, page * D, (uint32_t)page, 1)) != cudaSuccess) return e;
-    if ((e = attn::make_map(&tm_v, a.v, D, page, n, D, page * D, (uint32_t)page, 1)) != cudaSuccess) return e;
+    if ((e = attn::make_map(&tm_k, a.k, D, page, n, D, page * D, (uint32_t)std::min<uint64_t>(page, 64), 1)) != cudaSuccess) return e;
+    if ((e = attn::make_map(&tm_v, a.v, D, page, n, D, page * D, (uint32_t)std::min<uint64_t>(page, 64), 1)) != cudaSuccess) return e;
     *stage = "attn_prefix";
     auto kern = k_attn_prefill<D, true>;
     if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Layout<D>::SMEM)) != cudaSuccess)
