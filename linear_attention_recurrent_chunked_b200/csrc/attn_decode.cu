@@ -316,7 +316,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int i = 0; i < 4; ++i) s[t][i] += s2[t][i];
             // this lane: keys lane / 4 and lane / 4 + 8, heads 2 (lane % 4) and one more
             const bool in0 = (lane >> 2) < n, in1 = (lane >> 2) + 8 < n;
-            uint32_t pf[NT][2];
+            uint32_t pf[NT][2], pl[NT][2];
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
                 float mt[2], alpha[2];
@@ -346,9 +346,15 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                         for (int i = 0; i < 4; ++i) o[t][kk][i] *= alpha[i & 1];
                 }
-                // the weights enter the second product as bf16 (at most 2^-8 of each); l sums them unrounded
-                pf[t][0] = transpose8(tc::pack_bf16x2(s[t][0], s[t][1]));
-                pf[t][1] = transpose8(tc::pack_bf16x2(s[t][2], s[t][3]));
+                // the weights enter the second product as the sum of two bf16 values (within 2^-17 of each): the tensor
+                // pipe is idle here, and one value alone would add as much error as the output's own rounding has
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const uint32_t hi = tc::pack_bf16x2(s[t][2 * i], s[t][2 * i + 1]);
+                    pf[t][i] = transpose8(hi);
+                    pl[t][i] = transpose8(tc::pack_bf16x2(s[t][2 * i] - __uint_as_float(hi << 16),
+                                                          s[t][2 * i + 1] - __uint_as_float(hi & 0xFFFF0000u)));
+                }
             }
             const int vr = (lane & 7) + ((lane >> 4) << 3), vc = (lane >> 3) & 1;
 #pragma unroll
@@ -356,7 +362,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 uint32_t f[4];
                 ldmatrix4_t(vb + (kk >> 2) * (kStep * 128) + vr * 128 + (((2 * (kk & 3) + vc) ^ (vr & 7)) << 4), f);
 #pragma unroll
-                for (int t = 0; t < NT; ++t) mma16816(o[t][kk], f, pf[t][0], pf[t][1]);
+                for (int t = 0; t < NT; ++t) {
+                    mma16816(o[t][kk], f, pf[t][0], pf[t][1]);
+                    mma16816(o[t][kk], f, pl[t][0], pl[t][1]);
+                }
             }
             st = st + 1 == S::NST ? 0 : st + 1;
             phase ^= st == 0;

@@ -277,7 +277,7 @@ def _stream_and_ws(index, nbytes, workspace):
     and stream, or while a graph is being captured a fresh one, so that the graph keeps memory of its own."""
     stream = torch._C._cuda_getCurrentRawStream(index)
     if workspace is None:
-        if torch.cuda.is_current_stream_capturing():
+        if torch._C._cuda_isCurrentStreamCapturing():
             workspace = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=torch.device("cuda", index))
         else:
             workspace = _ws_cache.get((index, stream))
@@ -302,7 +302,7 @@ _NOTHING = _Nothing()
 
 def _on(index):
     """Makes the tensors' device the current one for a call, where it is not."""
-    return _NOTHING if index == torch.cuda.current_device() else torch.cuda.device(index)
+    return _NOTHING if index == torch._C._cuda_getDevice() else torch.cuda.device(index)
 
 
 _BF16, _I32, _FP32 = torch.bfloat16, torch.int32, torch.float32

@@ -191,6 +191,19 @@ def test_prefill_long_sequences_that_leave_a_query_tile_empty(G):
     close(want[b - lens[2]:b], ref, attn_tol(ref, a, q, k, 128, lens[2]))
 
 
+@pytest.mark.parametrize("N", [33, 128, 129, 300])
+def test_prefill_many_sequences(N):
+    """Sequence counts around those up to which blocks are placed by looking through the lengths."""
+    gen = torch.Generator().manual_seed(N)
+    lens = torch.randint(0, 90, (N,), generator=gen).tolist()
+    lens[N // 2] = 400
+    q, k, v, cu = prompt(gen, lens, 6, 2, 64)
+    v = v[:, 8:].contiguous()
+    o = gdn.attn_prefill(q.cuda(), k.cuda(), v.cuda(), cu.cuda(), max_len=500, check=True)
+    ref, a = al.prompt_attention(q, k, v, lens)
+    close(o, ref, attn_tol(ref, a, q, k, 64, 400))
+
+
 @pytest.mark.parametrize("trend", ["rising", "falling", "spikes"])
 @pytest.mark.parametrize("d", [64, 128])
 def test_prefill_moving_maximum(trend, d):
