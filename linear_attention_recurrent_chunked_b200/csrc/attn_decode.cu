@@ -558,6 +558,7 @@ __global__ void __launch_bounds__(128) k_attn_combine(const __grid_constant__ At
         for (int i = tid; i < kDecodeCtas; i += 128) found |= a.bad[i];
         const bool pages = __syncthreads_or(found & ERRBIT_PAGES), late = __syncthreads_or(found & ERRBIT_TIMEOUT),
                    internal = __syncthreads_or(found & ERRBIT_INTERNAL);
+        if (tid == 1) a.err[1] = 0u;
         if (tid == 0)
             *a.err = (a.prefix_len ? *a.err : 0u) | (pages ? ERRBIT_PAGES : 0u) | (late ? ERRBIT_TIMEOUT : 0u) |
                      (internal ? ERRBIT_INTERNAL : 0u);

@@ -173,7 +173,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
 
     Item it;
     if (PREFIX) {
-        if (blockIdx.x == 0 && tid == 0) *a.err = 0u;
+        if (blockIdx.x == 0 && tid < 2) a.err[tid] = 0u;
         asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the own keys' kernel needs nothing of this one
         const int b = blockIdx.x, rb = b / (a.Hkv * a.splits), rem = b - rb * a.Hkv * a.splits;
         it.head = rem / a.splits;
@@ -196,10 +196,10 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         it.split = 0;
         if (a.cu) {
             const bool bad = seqlens_bad(a);
-            if (blockIdx.x == 0 && tid == 0) *a.err = bad ? ERRBIT_SEQLENS : 0u;
+            if (blockIdx.x == 0 && tid < 2) a.err[tid] = bad && tid == 0 ? ERRBIT_SEQLENS : 0u;
             if (bad) return;
-        } else if (blockIdx.x == 0 && tid == 0) {
-            *a.err = 0u;
+        } else if (blockIdx.x == 0 && tid < 2) {
+            a.err[tid] = 0u;  // and the word that may say where a wait gave up
         }
         int t1;
         seq_bounds(a.cu, n, a.N, a.T_tot, it.t0, t1);

@@ -421,6 +421,15 @@ static bool stride_ok(int64_t stride, int T, int H, int d, int esize) {
     return (T <= 1 || stride >= (int64_t)H * d) && stride >= 0 && (stride * esize) % 16 == 0 &&
            (double)stride * std::max(T, 1) < 4.0e18 / esize;
 }
+// Whether a contiguous output of T tokens of Ho heads overlaps a [T][H][d] input; `in_place`: other than as the
+// whole of it, token for token.
+static bool overlaps(const void *out, int Ho, const void *in, int64_t stride, int H, int T, int d, int esize, bool in_place) {
+    if (!out || !in || T < 1) return false;
+    if (in_place && out == in && Ho == H && (T == 1 || stride == (int64_t)H * d)) return false;
+    const uintptr_t a = reinterpret_cast<uintptr_t>(out), b = reinterpret_cast<uintptr_t>(in);
+    const uintptr_t an = (uintptr_t)T * Ho * d * esize, bn = ((uintptr_t)(T - 1) * stride + (uintptr_t)H * d) * esize;
+    return a < b + bn && b < a + an;
+}
 static bool page_size_ok(int p) { return p == 16 || p == 32 || p == 64 || p == 128; }
 
 gdn_status gdn_qk_norm_rope(const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v,
@@ -456,6 +465,13 @@ gdn_status gdn_qk_norm_rope(const void *q, int64_t q_stride, const void *k, int6
     if (!workspace || ws_bytes < kErrWordBytes)
         return fail(GDN_ERR_WORKSPACE, "workspace of at least %zu bytes (the error word) needed", kErrWordBytes);
     if ((reinterpret_cast<uintptr_t>(workspace) & 3u) != 0) return fail(GDN_ERR_ALIGN, "workspace must be 4-byte aligned");
+    if (overlaps(q_out, Hq, q, q_stride, Hq, T, d, es, true) || overlaps(q_out, Hq, k, k_stride, Hkv, T, d, es, false) ||
+        overlaps(k_out, Hkv, k, k_stride, Hkv, T, d, es, true) || overlaps(k_out, Hkv, q, q_stride, Hq, T, d, es, false) ||
+        overlaps(k_out, Hkv, q_out, (int64_t)Hq * d, Hq, T, d, es, false) ||
+        (slots && (overlaps(q_out, Hq, v, v_stride, Hkv, T, d, es, false) ||
+                   overlaps(k_out, Hkv, v, v_stride, Hkv, T, d, es, false))))
+        return fail(GDN_ERR_SHAPE, "q_out and k_out may be contiguous q and k themselves, but not overlap the inputs or each "
+                    "other otherwise");
     const gdn::NormRope a{q, k, v, q_stride, k_stride, v_stride, wq, wk, eps, positions, T, Hq, Hkv, rot, base,
                           q_out, k_out, k_cache, v_cache, slots, num_pages, page_size, static_cast<uint32_t *>(workspace)};
     const cudaError_t e = gdn::launch_norm_rope(a, d, dtype == GDN_BF16, static_cast<cudaStream_t>(stream));
@@ -493,6 +509,9 @@ gdn_status gdn_attn_prefill(const void *q, int64_t q_stride, const void *k, int6
     if (!workspace || ws_bytes < kErrWordBytes)
         return fail(GDN_ERR_WORKSPACE, "workspace of at least %zu bytes (the error word) needed", kErrWordBytes);
     if ((reinterpret_cast<uintptr_t>(workspace) & 3u) != 0) return fail(GDN_ERR_ALIGN, "workspace must be 4-byte aligned");
+    if (overlaps(o, Hq, q, q_stride, Hq, T_tot, d, 2, false) || overlaps(o, Hq, k, k_stride, Hkv, T_tot, d, 2, false) ||
+        overlaps(o, Hq, v, v_stride, Hkv, T_tot, d, 2, false))
+        return fail(GDN_ERR_SHAPE, "o overlaps q, k or v");
     if (!(scale > 0.f)) scale = 1.f / sqrtf((float)d);
     gdn::AttnPrefill a{};
     a.q = static_cast<const __nv_bfloat16 *>(q);
@@ -565,6 +584,7 @@ gdn_status gdn_attn_decode(const void *q, const void *k_cache, const void *v_cac
     if ((reinterpret_cast<uintptr_t>(page_table) | reinterpret_cast<uintptr_t>(lens) |
          reinterpret_cast<uintptr_t>(prefix_pages)) & 3u)
         return fail(GDN_ERR_ALIGN, "page_table, lens and prefix_pages must be 4-byte aligned");
+    if (overlaps(o, Hq, q, (int64_t)Hq * d, Hq, B, d, 2, false)) return fail(GDN_ERR_SHAPE, "o overlaps q");
     const DecodeWs w(B, Hq, Hkv, d, prefix_len);
     if (!workspace || ws_bytes < w.total)
         return fail(GDN_ERR_WORKSPACE, "workspace of %zu bytes given, %zu needed", workspace ? ws_bytes : 0, w.total);

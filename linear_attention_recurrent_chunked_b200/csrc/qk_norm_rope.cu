@@ -104,7 +104,7 @@ __global__ void __launch_bounds__(kWarps * 32, kResident) k_norm_rope(const __gr
             for (int t = threadIdx.x; t < a.T; t += kWarps * 32) bad |= a.slots[t] < -1 || a.slots[t] >= lim;
         }
         bad = __syncthreads_or(bad);
-        if (threadIdx.x == 0) *a.err = bad ? ERRBIT_PAGES : 0u;
+        if (threadIdx.x < 2) a.err[threadIdx.x] = bad && threadIdx.x == 0 ? ERRBIT_PAGES : 0u;
         return;
     }
     __shared__ uint64_t freq[64];

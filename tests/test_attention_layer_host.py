@@ -19,6 +19,11 @@ def lib():
     return gdn.load_library()
 
 
+def apart(args):
+    """The fake pointers of a call, each with 16 GB of its own."""
+    return {n: (VP((1 << 40) + i * (1 << 34)) if v is FAKE else v) for i, (n, v) in enumerate(args.items())}
+
+
 ROPE = dict(q=FAKE, qs=16 * 128, k=FAKE, ks=4 * 128, v=FAKE, vs=4 * 128, wq=FAKE, wk=FAKE, eps=1e-6, positions=FAKE, T=8,
             Hq=16, Hkv=4, d=128, rot=128, base=1e4, dt=1, q_out=FAKE, k_out=FAKE, k_cache=FAKE, v_cache=FAKE, slots=FAKE,
             pages=8, page=16, ws=FAKE, ws_bytes=256, stream=None)
@@ -37,7 +42,7 @@ ROPE = dict(q=FAKE, qs=16 * 128, k=FAKE, ks=4 * 128, v=FAKE, vs=4 * 128, wq=FAKE
     (dict(ws=None), 6), (dict(ws_bytes=255), 6), (dict(ws=ODD), 4),
 ])
 def test_qk_norm_rope_refuses(lib, over, status):
-    assert lib.gdn_qk_norm_rope(*{**ROPE, **over}.values()) == status
+    assert lib.gdn_qk_norm_rope(*{**apart(ROPE), **over}.values()) == status
     assert lib.gdn_last_error()
 
 
@@ -54,8 +59,29 @@ PREFILL = dict(q=FAKE, qs=16 * 128, k=FAKE, ks=4 * 128, v=FAKE, vs=4 * 128, cu=F
     (dict(cu=ODD), 4), (dict(ws=None), 6), (dict(ws_bytes=100), 6), (dict(ws=ODD), 4),
 ])
 def test_attn_prefill_refuses(lib, over, status):
-    assert lib.gdn_attn_prefill(*{**PREFILL, **over}.values()) == status
+    assert lib.gdn_attn_prefill(*{**apart(PREFILL), **over}.values()) == status
     assert lib.gdn_last_error()
+
+
+def at(offset):
+    return VP((1 << 30) + offset)
+
+
+@pytest.mark.parametrize("call,base,over", [
+    # decode: o on q, and next to it
+    ("gdn_attn_decode", "DECODE", dict(q=at(0), o=at(0))),
+    ("gdn_attn_decode", "DECODE", dict(q=at(0), o=at(4 * 16 * 128 * 2 - 16))),
+    # prefill: o on a key slice of a fused buffer that q shares
+    ("gdn_attn_prefill", "PREFILL", dict(q=at(0), qs=2560, k=at(4096), ks=2560, o=at(8192))),
+    # rope: in place is fine for whole tensors only
+    ("gdn_qk_norm_rope", "ROPE", dict(q=at(0), q_out=at(256))),
+    ("gdn_qk_norm_rope", "ROPE", dict(q=at(0), qs=25 * 128, q_out=at(0))),
+    ("gdn_qk_norm_rope", "ROPE", dict(k=at(0), q_out=at(0))),
+    ("gdn_qk_norm_rope", "ROPE", dict(q_out=at(0), k_out=at(16))),
+])
+def test_overlapping_outputs_are_refused(lib, call, base, over):
+    assert getattr(lib, call)(*{**apart(globals()[base]), **over}.values()) == 2
+    assert b"overlap" in lib.gdn_last_error()
 
 
 def test_binding_refuses(lib):
@@ -93,7 +119,7 @@ DECODE = dict(q=FAKE, kc=FAKE, vc=FAKE, pages=64, page=16, table=FAKE, max_pages
     (dict(prefix_pages=ODD), 4), (dict(ws=None), 6), (dict(ws_bytes=256), 6), (dict(ws=VP((1 << 20) + 16)), 4),
 ])
 def test_attn_decode_refuses(lib, over, status):
-    assert lib.gdn_attn_decode(*{**DECODE, **over}.values()) == status
+    assert lib.gdn_attn_decode(*{**apart(DECODE), **over}.values()) == status
     assert lib.gdn_last_error()
 
 
@@ -105,7 +131,7 @@ def test_attn_decode_workspace_size(lib):
     assert size(64, 16, 4, 128, 8192) >= plain + 64 * 16 * 130 * 4 * 2
     assert size(0, 16, 4, 128, 0) == 256  # refused by the call
     # a byte less than it says is refused
-    assert lib.gdn_attn_decode(*{**DECODE, "ws_bytes": size(4, 16, 4, 128, 100) - 1}.values()) == 6
+    assert lib.gdn_attn_decode(*{**apart(DECODE), "ws_bytes": size(4, 16, 4, 128, 100) - 1}.values()) == 6
 
 
 def test_binding_refuses_decode(lib):
