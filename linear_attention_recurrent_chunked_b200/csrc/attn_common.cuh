@@ -51,6 +51,27 @@ __device__ __noinline__ inline void drain_bar(uint64_t *bar, uint32_t parity) {
         if (tc::globaltimer() - t0 > kWaitNs) return;
 }
 
+// Every kernel here is launched to start while the one before it in the stream drains (launch_early): it sets
+// up what is its own, then waits here for that one's end before it touches global memory.
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// The next kernel may start. (Its own wait still waits for this kernel's end.)
+__device__ __forceinline__ void grid_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+template <typename K, typename... A>
+inline cudaError_t launch_early(K kern, unsigned grid, unsigned threads, size_t smem, cudaStream_t st, const A &...args) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
 // Two fp32 values in one 64-bit register pair, for the packed fp32 instructions.
 __device__ __forceinline__ uint64_t pack2(float a, float b) {
     uint64_t r;

@@ -35,6 +35,8 @@ namespace {
 
 using bf16 = __nv_bfloat16;
 using attn::Ctl;
+using attn::grid_launch_dependents;
+using attn::grid_wait;
 constexpr int kWarps = 8, kThreads = kWarps * 32;
 constexpr int kStep = 16;                // keys of a step
 constexpr int kRuns = kDecodeCtas * kWarps;
@@ -76,9 +78,6 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-__device__ __forceinline__ void grid_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-
 __device__ __forceinline__ int length_of(const AttnDecode &a, int b) {
     return min(max(a.lens[b], 0), a.max_pages << a.page_log);  // max_pages << page_log is at most 2^30
 }
@@ -152,7 +151,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                   const __grid_constant__ AttnDecode a) {
     using S = Smem<D, NT>;
     extern __shared__ __align__(1024) uint8_t smem[];
-    grid_launch_dependents();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t ring = tc::smem_u32(smem) + warp * S::RING;
     float2 *const piece_ml = reinterpret_cast<float2 *>(smem + S::OFF_ML);  // [2 warp + (0 first, 1 last)][heads]
@@ -169,6 +167,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (tid == 0) ctl.abort = 0;
+    // with a prefix its kernel comes before, whose CTAs have all waited already and whose results nothing here reads
+    if (!a.prefix_len) grid_wait();
+    grid_launch_dependents();
 
     if (ring & 1023u) {  // the boxes' swizzle counts on it
         if (tid == 0) a.bad[blockIdx.x] = ERRBIT_INTERNAL;
@@ -637,21 +638,6 @@ __global__ void __launch_bounds__(128) k_attn_combine(const __grid_constant__ At
         make_uint2(tc::pack_bf16x2(x.x * inv, x.y * inv), tc::pack_bf16x2(x.z * inv, x.w * inv));
 }
 
-template <typename K, typename... A>
-cudaError_t launch_pdl(K kern, unsigned grid, unsigned threads, size_t smem, cudaStream_t st, bool early, const A &...args) {
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3(threads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = st;
-    cudaLaunchAttribute at{};
-    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &at;
-    cfg.numAttrs = early ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, kern, args...);
-}
-
 template <int D, int NT>
 cudaError_t launch(AttnDecode a, cudaStream_t st, const char **stage) {
     cudaError_t e;
@@ -665,12 +651,12 @@ cudaError_t launch(AttnDecode a, cudaStream_t st, const char **stage) {
     constexpr size_t smem = Smem<D, NT>::TOTAL;
     if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) != cudaSuccess) return e;
     void *pr = prof_start("attn_decode", st);
-    e = launch_pdl(kern, kDecodeCtas, kThreads, smem, st, a.prefix_len > 0, tm_k, tm_v, a);
+    e = attn::launch_early(kern, kDecodeCtas, kThreads, smem, st, tm_k, tm_v, a);
     prof_stop(pr);
     if (e != cudaSuccess) return e;
     *stage = "attn_combine";
     pr = prof_start("attn_combine", st);
-    e = launch_pdl(k_attn_combine<D>, (unsigned)((int64_t)a.B * a.Hq), 128, 0, st, true, a);
+    e = attn::launch_early(k_attn_combine<D>, (unsigned)((int64_t)a.B * a.Hq), 128, 0, st, a);
     prof_stop(pr);
     return e;
 }

@@ -171,10 +171,11 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const int P = a.P;
 
+    attn::grid_wait();
+    attn::grid_launch_dependents();  // the kernel of the own keys needs nothing of a prefix's
     Item it;
     if (PREFIX) {
         if (blockIdx.x == 0 && tid < 2) a.err[tid] = 0u;
-        asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the own keys' kernel needs nothing of this one
         const int b = blockIdx.x, rb = b / (a.Hkv * a.splits), rem = b - rb * a.Hkv * a.splits;
         it.head = rem / a.splits;
         it.split = rem - it.head * a.splits;
@@ -485,9 +486,9 @@ cudaError_t launch_prompt(AttnPrefill a, cudaStream_t st, const char **stage) {
     if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Layout<D>::SMEM)) != cudaSuccess)
         return e;
     void *pr = prof_start("attn_prefill", st);
-    kern<<<a.blocks * a.Hkv * a.N, NTHREADS, Layout<D>::SMEM, st>>>(tm_q, tm_k, tm_v, a);
+    e = attn::launch_early(kern, (unsigned)(a.blocks * a.Hkv * a.N), NTHREADS, Layout<D>::SMEM, st, tm_q, tm_k, tm_v, a);
     prof_stop(pr);
-    return cudaGetLastError();
+    return e;
 }
 
 template <int D>
@@ -506,9 +507,9 @@ cudaError_t launch_prefix(AttnPrefill a, cudaStream_t st, const char **stage) {
     if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Layout<D>::SMEM)) != cudaSuccess)
         return e;
     void *pr = prof_start("attn_prefix", st);
-    kern<<<a.blocks * a.Hkv * a.splits, NTHREADS, Layout<D>::SMEM, st>>>(tm_q, tm_k, tm_v, a);
+    e = attn::launch_early(kern, (unsigned)(a.blocks * a.Hkv * a.splits), NTHREADS, Layout<D>::SMEM, st, tm_q, tm_k, tm_v, a);
     prof_stop(pr);
-    return cudaGetLastError();
+    return e;
 }
 
 }  // namespace

@@ -96,6 +96,10 @@ template <typename T, int D>
 __global__ void __launch_bounds__(kWarps * 32, kResident) k_norm_rope(const __grid_constant__ Args p, const __grid_constant__ Freq fr) {
     constexpr int E = Run<T>::E, LPR = D / (2 * E), RPW = 32 / LPR;  // elements of a run, lanes per row, rows per group
     const NormRope &a = p.a;
+    __shared__ uint64_t freq[64];
+    if (threadIdx.x < a.rot / 2) freq[threadIdx.x] = fr.f[threadIdx.x];
+    attn::grid_wait();
+    attn::grid_launch_dependents();
     if (blockIdx.x == 0) {
         bool bad = false;
         if (a.slots) {
@@ -107,8 +111,6 @@ __global__ void __launch_bounds__(kWarps * 32, kResident) k_norm_rope(const __gr
         if (threadIdx.x < 2) a.err[threadIdx.x] = bad && threadIdx.x == 0 ? ERRBIT_PAGES : 0u;
         return;
     }
-    __shared__ uint64_t freq[64];
-    if (threadIdx.x < a.rot / 2) freq[threadIdx.x] = fr.f[threadIdx.x];
     __syncthreads();
     const int64_t w = (int64_t)(blockIdx.x - 1) * kWarps + (threadIdx.x >> 5);
     if (w >= p.warps) return;
@@ -280,9 +282,9 @@ cudaError_t launch(const NormRope &a, cudaStream_t st) {
     for (int i = 0; i < a.rot / 2; ++i, f *= step) fr.f[i] = (uint64_t)(f + 0.5L);
     const unsigned grid = (unsigned)((p.warps + kWarps - 1) / kWarps) + 1;
     void *pr = prof_start("qk_norm_rope", st);
-    k_norm_rope<T, D><<<grid, kWarps * 32, 0, st>>>(p, fr);
+    const cudaError_t e = attn::launch_early(k_norm_rope<T, D>, grid, kWarps * 32, 0, st, p, fr);
     prof_stop(pr);
-    return cudaGetLastError();
+    return e;
 }
 
 }  // namespace

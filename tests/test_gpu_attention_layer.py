@@ -511,3 +511,48 @@ def test_layer_prompt_then_steps(d, rot):
     tol = attn_tol(ref, a, q, k, d, max(have))
     close(full[ends - 1], ref[ends - 1], tol[ends - 1])
     close(o, ref[ends - 1], tol[ends - 1])
+
+
+def test_layer_chain_without_gaps_and_in_a_graph():
+    """The operators back to back on one stream, each reading what the one before has just written and
+    starting while that one drains; eagerly many times over and in one captured graph with other work
+    between them: the same bits as with the device idle in between."""
+    gen = torch.Generator().manual_seed(31)
+    Hq, Hkv, d, page, B = 8, 2, 128, 16, 40
+    x = randn(gen, B, Hq + 2 * Hkv, d).cuda()
+    pos = torch.full((B,), 99, dtype=torch.int32, device="cuda")
+    w = on_gpu(cached(gen, [100] * B, Hq, Hkv, d, page, 200, stale=0.0))
+    slots = (w["page_table"][:, 6] * page + 3).to(torch.int32)  # key 99 of each
+    k0, v0 = w["k_cache"].clone(), w["v_cache"].clone()
+
+    def chain(sync, o):
+        w["k_cache"].copy_(k0)
+        w["v_cache"].copy_(v0)
+        for i in range(3):
+            sync()
+            q, _ = gdn.qk_norm_rope(x[:, :Hq], x[:, Hq:Hq + Hkv], None, None, pos, v=x[:, Hq + Hkv:], k_cache=w["k_cache"],
+                                    v_cache=w["v_cache"], slots=slots, want_k=False)
+            sync()
+            y = gdn.attn_decode(q, w["k_cache"], w["v_cache"], w["page_table"], w["lens"], w["prefix_pages"] if i else None, 200 if i else 0)
+            sync()
+            z = gdn.attn_prefill(y, x[:, Hq:Hq + Hkv], x[:, Hq + Hkv:])
+            sync()
+            o[i].copy_(z)
+            x[:, :Hq].copy_(z)
+        x[:, :Hq].copy_(x0)
+
+    x0 = x[:, :Hq].clone()
+    want, got = (torch.zeros((3, B, Hq, d), dtype=BF, device="cuda") for _ in range(2))
+    chain(torch.cuda.synchronize, want)
+    torch.cuda.synchronize()
+    for _ in range(10):
+        chain(lambda: None, got)
+        assert torch.equal(got, want)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        chain(lambda: None, got)
+    for _ in range(5):
+        got.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(got, want)
