@@ -102,28 +102,6 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     return r;
 }
 
-// 2^x of two values on the FMA and integer pipes, for x <= 120; from -127 down exactly 0. x = n + f with n
-// the nearest integer (adding 1.5 2^23 leaves it in the low mantissa bits), 2^f by the polynomial of
-// degree 4 with constant term 1 whose largest relative error on [-1/2, 1/2] is smallest (2.9e-6 in
-// fp32, found by iteratively reweighted least squares), and n added to the exponent.
-__device__ __forceinline__ void exp2_poly(uint64_t x, float &r0, float &r1) {
-    float x0, x1;
-    unpack2(x, x0, x1);
-    x = pack2(fmaxf(x0, -127.f), fmaxf(x1, -127.f));
-    const uint64_t t = add2(x, pack2(12582912.f, 12582912.f));
-    const uint64_t n = add2(t, pack2(-12582912.f, -12582912.f));
-    const uint64_t f = fma2(n, pack2(-1.f, -1.f), x);
-    uint64_t p = fma2(f, pack2(0.009582852944731712f, 0.009582852944731712f), pack2(0.055906426161527634f, 0.055906426161527634f));
-    p = fma2(f, p, pack2(0.24024099111557007f, 0.24024099111557007f));
-    p = fma2(f, p, pack2(0.6931241750717163f, 0.6931241750717163f));
-    p = fma2(f, p, pack2(1.f, 1.f));
-    float t0, t1, p0, p1;
-    unpack2(t, t0, t1);
-    unpack2(p, p0, p1);
-    r0 = __uint_as_float((__float_as_uint(t0) << 23) + __float_as_uint(p0));
-    r1 = __uint_as_float((__float_as_uint(t1) << 23) + __float_as_uint(p1));
-}
-
 // Eight fp32 values to a 32-byte aligned place: a whole sector from one thread.
 __device__ __forceinline__ void st_global8(float *p, const float *x) {
     asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(__float_as_uint(x[0])),
@@ -144,15 +122,6 @@ __device__ __forceinline__ void tmem_ld32x(uint32_t taddr, uint32_t (&u)[32]) {
         : "r"(taddr)
         : "memory");
 }
-// Registers -> TMEM, 16 consecutive columns.
-__device__ __forceinline__ void tmem_st16x(uint32_t taddr, const uint32_t (&u)[16]) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
-        "r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7]), "r"(u[8]), "r"(u[9]),
-        "r"(u[10]), "r"(u[11]), "r"(u[12]), "r"(u[13]), "r"(u[14]), "r"(u[15])
-        : "memory");
-}
-
 // TMA descriptor of a bf16 tensor [n2][n1][n0] with n0 contiguous and the given strides (elements,
 // multiples of 8); boxes of 64 x b1 x b2 elements written with the 128-byte swizzle, places outside
 // the tensor reading as zero.

@@ -6,28 +6,30 @@
 // A tile of 128 query rows packs P = floor(128 / G) consecutive positions times the G query heads of
 // one key head, position-major, which is the order in which one TMA box {64 columns, G heads,
 // P positions} lands. All rows of a tile then share their key and value tiles whatever G is, and a
-// tile's causal edge is P positions long. Per key tile of 128 keys
+// tile's causal edge is P positions long. Per step of 64 keys
 //
-//     S = Q K^T (tensor memory)  ->  P = 2^(S c - m) (bf16, over S)  ->  O += P V (tensor memory)
+//     S = Q K^T (tensor memory)  ->  P = 2^(S c - m) (bf16, tensor memory)  ->  O += P V (tensor memory)
 //
 // with c = scale log2(e) and m a running row maximum that moves only when the true one has grown by
 // more than 8, so P <= 2^8 and O and the row sum l are seldom rescaled; o = O / l. P is rounded to
 // bf16 for the tensor core (at most 2^-8 of each weight); l sums the unrounded weights in fp32.
 //
-// One CTA holds two tiles (256 rows), and S comes in steps of 64 keys with two buffers per tile: the
-// softmax of one step of a tile runs while the tensor core computes the tile's next S and the other
-// tile's products. Roles:
-//   softmax  (2 x 4 warps)  one query row per thread
-//   loader   (1 warp)       TMA: Q once, then K and V tiles of 128 keys through one ring
-//   MMA      (1 warp)       per step and query tile: O += P V; then, one product later, the S two steps on
-//                           into the buffer that P was in, once that product has read P (a later
-//                           tcgen05.mma is not ordered after an earlier one's tensor-memory operand reads)
-// Bound: the tensor pipe. A step of a tile costs 8 products M=128 N=64 K=16 for S, whose operands both
-// come from shared memory (6 KB each at 128 bytes a cycle: 48 cycles, against 32 of arithmetic), and
-// 4 products M=128 N=128 K=16 for O (64 cycles each, V alone from shared memory): 640 cycles. With steps
-// of 128 keys S would run at its arithmetic rate (1024 cycles for twice the keys), but tensor memory then
-// holds one S buffer per tile beside O, and the chain S -> maximum -> weights -> O -> next S (4,250
-// cycles measured, half of it barrier and tensor-memory latencies) sets the pace instead.
+// One CTA holds one tile and goes through the keys in steps of 64. Its steps are a chain (S -> maximum ->
+// weights -> O), so two CTAs share an SM and one's softmax runs beside the other's products. Roles:
+//   softmax  (4 warps)  one query row per thread: no exchange between lanes
+//   loader   (1 warp)   TMA: Q once, then K and V tiles of 64 keys, by turns, through one ring of five
+//   S        (1 warp)   S = Q K^T as soon as the softmax has S of the step before in registers
+//   O        (1 warp)   O += P V as soon as the weights are written
+// Weights have their own tensor memory beside S, so that the next S does not wait for O += P V; with O that
+// is 224 of the CTA's 256 columns, and the last 32 hold 64 of Q's columns: those products of S take one operand
+// from shared memory instead of two (32 cycles of 128x64x16 against 48 at 128 bytes a cycle).
+// Bound: the chain of a step and the tensor pipe together. At 4,096 tokens, 16/4 heads, d = 128: 68.4 us,
+// tensor pipe 57 %, exponentials (MUFU) 57 %, issue slots 38 %. One sequence of 10,240 tokens, 16/4 heads: 345 us in
+// short runs, 373 us over seconds (power limit): 1,245 and 1,150 TFLOP/s, against 1,656 and 1,470 of a library bf16
+// product of the same machine. The same prompt on the way here, in short runs: two tiles in one CTA, whose softmax
+// warps fall into lockstep, 361 us (with two threads per row 403, with steps of 128 keys, where P lies over S, 391);
+// one tile per CTA 349, with a quarter of the exponentials as polynomials on the FMA pipe 353, with Q's columns in
+// tensor memory 345.
 // Key tiles are counted from the sequence's start (or the prefix split's), so a tile may reach past
 // the end into another sequence's rows or stale cache slots; their weights are zero, and their V rows
 // are overwritten with zeros in shared memory before the product, so that a NaN there stays there.
@@ -35,7 +37,6 @@
 #include <math.h>
 
 #include <algorithm>
-#include <type_traits>
 
 #include "attn_common.cuh"
 #include "chunk_common.cuh"
@@ -45,37 +46,35 @@ namespace gdn {
 namespace {
 
 using attn::Ctl;
-using attn::wait_bar;
 using attn::wait_bar_w;
 using bf16 = __nv_bfloat16;
 
-constexpr int TQ = 128, TK = 128;   // query rows of a tile, keys of a K or V tile in the ring
-constexpr int STEP = 64;            // keys of a step: half a ring tile
-constexpr float kRescale = 8.f;  // log2 units
-constexpr int NTHREADS = 416;
-constexpr int W_LOAD = 8, W_MMA = 9;
+constexpr int TQ = 128, STEP = 64;  // query rows of a tile, keys of a step and of a K or V tile in the ring
+constexpr float kRescale = 8.f;     // log2 units
+constexpr int NTHREADS = 224;       // four softmax warps, the loader, S and O
+constexpr int W_LOAD = 4, W_S = 5;  // and O's
 
 template <int D>
 struct Layout {
-    static constexpr uint32_t TILE = 128 * D * 2;      // D / 64 column blocks of 128 rows x 128 bytes
-    static constexpr int NST = D == 128 ? 5 : 8;       // K and V tiles in the ring
-    static constexpr uint32_t OFF_Q = 0, OFF_KV = 2 * TILE, OFF_BAR = OFF_KV + NST * TILE;
-    // barriers: Q landed, ring full / empty, per query tile: S complete, S read, P written, O += P V done, Q in
-    // tensor memory; the first weights of tile 0; all products done
-    static constexpr int QFULL = 0, FULL = 1, EMPTY = FULL + NST, SFULL = EMPTY + NST, SFREE = SFULL + 2,
-                         PREADY = SFREE + 2, QT = PREADY + 2, START = QT + 2, PVD = START + 1, FIN = PVD + 2, NBAR = FIN + 1;
+    static constexpr uint32_t QTILE = TQ * D * 2;   // D / 64 column blocks of 128 rows x 128 bytes
+    static constexpr uint32_t KTILE = STEP * D * 2; // D / 64 column blocks of 64 rows x 128 bytes
+    static constexpr uint32_t QBLOCK = TQ * 128, KBLOCK = STEP * 128;
+    static constexpr int NST = 5;                   // K and V tiles in the ring: K of step j is tile 2 j, V tile 2 j + 1
+    static constexpr uint32_t OFF_Q = 0, OFF_KV = QTILE, OFF_BAR = OFF_KV + NST * KTILE;
+    // barriers: Q landed, ring full / empty, S complete, S read, P written, O += P V done, Q in tensor memory; all
+    // products done
+    static constexpr int QFULL = 0, FULL = 1, EMPTY = FULL + NST, SFULL = EMPTY + NST, SFREE = SFULL + 1, PREADY = SFREE + 1,
+                         QT = PREADY + 1, PVD = QT + 1, FIN = PVD + 1, NBAR = FIN + 1;
     static constexpr uint32_t OFF_CTL = OFF_BAR + 8 * NBAR;
-    static constexpr uint32_t SMEM = OFF_CTL + 16 + 1024;
-    // tensor memory columns: S of tile u at u * 64, P at 128 + u * 32, Q of the first QT_TILES tiles, O at 256 + u * D
-    static constexpr uint32_t TM_S = 0, TM_P = 128, TM_Q = 192, TM_O = 256;
-    static constexpr int QT_TILES = 128 / D;
-    static constexpr int POLY = D == 64 ? 2 : 0;       // of every 8 weights, those that the FMA pipe computes: see the softmax
+    static constexpr uint32_t SMEM = OFF_CTL + 16;
+    // tensor memory columns, 256 of them: S, P, 64 columns of Q, O
+    static constexpr uint32_t TM_S = 0, TM_P = 64, TM_Q = 96, TM_O = 128;
 };
 
-// What a CTA works on: query positions [pos0, pos0 + 2 P) of a sequence of `len` from token t0 on, ns0 and
-// ns1 steps of its two query tiles (ns1 is 0 or at least ns0) over the keys from k0 on, `keys` of them there.
+// What a CTA works on: query positions [pos0, pos0 + P) of a sequence of `len` from token t0 on, `ns` steps
+// over the keys from k0 on, `keys` of them there.
 struct Item {
-    int t0, len, pos0, head, k0, keys, ns0, ns1, split;
+    int t0, len, pos0, head, k0, keys, ns, split;
 };
 
 // cu_seqlens malformed: the same answer from every thread of the CTA.
@@ -89,82 +88,67 @@ __device__ __forceinline__ bool seqlens_bad(const AttnPrefill &a) {
     return __syncthreads_or(bad);
 }
 
-// The ring holds K of steps 2 t and 2 t + 1 as tile 2 t, V of them as tile 2 t + 1. A tile is freed by two
-// arrivals, one for each query tile: the commit of that query tile's last product on it, or the loader's own
-// where it has none. A warp waits only for the tiles that it uses, K or V: a parity wait then is good only
-// because the tile before in the same stage (of the other kind) has certainly landed, as the same query
-// tile's earlier products read it.
+// A warp waits only for the ring tiles that it uses, K or V, each freed by the commit of its product. A wait by
+// parity then is good only because the tile before in the same stage (of the other kind) has certainly landed: it
+// follows the wait that shows it, as said at each.
 template <int D>
 __device__ __forceinline__ bool ring_full(uint64_t *bar, int c, Ctl *ctl, uint32_t *err) {
     using L = Layout<D>;
     return wait_bar_w(&bar[L::FULL + c % L::NST], (uint32_t)((c / L::NST) & 1), ctl, err);
 }
 
-// S of query tile U, issued by a warp of its own. The second tile starts when the first has its first
-// weights, which keeps the two tiles about half a step apart: in step they would wait for the MUFU and the
-// tensor core together and leave both idle together (10k prompt: 391 us in step, 352 us apart).
-template <int D, int U>
-__device__ __forceinline__ void s_loop(std::integral_constant<int, U> u, int myns, uint32_t tm, uint32_t sb,
-                                       uint64_t *bar, Ctl *ctl, uint32_t *err) {
+template <int D>
+__device__ __forceinline__ void s_loop(int ns, uint32_t tm, uint32_t sb, uint64_t *bar, Ctl *ctl, uint32_t *err) {
     using L = Layout<D>;
     const uint32_t id_s = tc::make_idesc_bf16(TQ, STEP, 0, 0);  // both operands K-major
-    const tc::Desc dq = tc::split_desc(tc::make_desc_sw128(sb + L::OFF_Q + u * L::TILE, 16, 1024));
+    const tc::Desc dq = tc::split_desc(tc::make_desc_sw128(sb + L::OFF_Q, 16, 1024));
     const tc::Desc dk = tc::split_desc(tc::make_desc_sw128(sb + L::OFF_KV, 16, 1024));
-    constexpr bool TS = U < L::QT_TILES;
-    bool ok = myns == 0 || wait_bar_w(&bar[TS ? L::QT + U : L::QFULL], 0, ctl, err);
-    if (ok && U == 1 && myns > 0) ok = wait_bar_w(&bar[L::START], 0, ctl, err);
-    for (int j = 0; ok && j < myns; ++j) {
-        const int c = j & ~1;
-        if (!(ok = ((j & 1) || ring_full<D>(bar, c, ctl, err)) &&
-                   (j == 0 || wait_bar_w(&bar[L::SFREE + u], (uint32_t)((j - 1) & 1), ctl, err))))
+    bool ok = wait_bar_w(&bar[L::QFULL], 0, ctl, err) && wait_bar_w(&bar[L::QT], 0, ctl, err);
+    for (int j = 0; ok && j < ns; ++j) {
+        // S of step j - 1 read: the weights of step j - 2 are written, so O has taken V of step j - 3, ring tile 2 j - 5
+        if (!(ok = (j == 0 || wait_bar_w(&bar[L::SFREE], (uint32_t)((j - 1) & 1), ctl, err)) && ring_full<D>(bar, 2 * j, ctl, err)))
             break;
         tc::fence_after_sync();
-        const uint32_t kb = (uint32_t)(c % L::NST) * L::TILE + (j & 1) * (STEP * 128);
+        const uint32_t kb = (uint32_t)(2 * j % L::NST) * L::KTILE;
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
-            const uint32_t off = (kk >> 2) * 16384 + (kk & 3) * 32;
-            if (TS)
-                tc::mma_bf16_ts_off_w(tm + L::TM_S + u * 64, tm + L::TM_Q + u * (D / 2) + 8 * kk, dk, kb + off, id_s, kk > 0);
+            const uint32_t q = (kk >> 2) * L::QBLOCK + (kk & 3) * 32, k = kb + (kk >> 2) * L::KBLOCK + (kk & 3) * 32;
+            if (kk < 4)
+                tc::mma_bf16_ts_off_w(tm + L::TM_S, tm + L::TM_Q + 8 * kk, dk, k, id_s, kk > 0);
             else
-                tc::mma_bf16_off_w(tm + L::TM_S + u * 64, dq, off, dk, kb + off, id_s, kk > 0);
+                tc::mma_bf16_off_w(tm + L::TM_S, dq, q, dk, k, id_s, kk > 0);
         }
-        tc::mma_commit_w(&bar[L::SFULL + u]);
-        if ((j & 1) || j + 1 == myns) tc::mma_commit_w(&bar[L::EMPTY + c % L::NST]);
+        tc::mma_commit_w(&bar[L::SFULL]);
+        tc::mma_commit_w(&bar[L::EMPTY + 2 * j % L::NST]);
     }
 }
 
-// O of query tile u, issued by a warp of its own.
-template <int D, int U>
-__device__ __forceinline__ void pv_loop(std::integral_constant<int, U> u, int myns, uint32_t tm, uint32_t sb,
-                                        uint64_t *bar, Ctl *ctl, uint32_t *err) {
+template <int D>
+__device__ __forceinline__ void o_loop(int ns, uint32_t tm, uint32_t sb, uint64_t *bar, Ctl *ctl, uint32_t *err) {
     using L = Layout<D>;
     const uint32_t id_o = tc::make_idesc_bf16(TQ, D, 0, 1);  // V MN-major
-    const tc::Desc dv = tc::split_desc(tc::make_desc_sw128(sb + L::OFF_KV, 16384, 1024));
+    const tc::Desc dv = tc::split_desc(tc::make_desc_sw128(sb + L::OFF_KV, L::KBLOCK, 1024));
     bool ok = true;
-    for (int j = 0; ok && j < myns; ++j) {
-        const int b = j & 1, c = j | 1;
-        if (!(ok = (b || ring_full<D>(bar, c, ctl, err)) &&
-                   wait_bar_w(&bar[L::PREADY + u], (uint32_t)(j & 1), ctl, err)))
-            break;
+    for (int j = 0; ok && j < ns; ++j) {
+        const int c = 2 * j + 1;
+        // the weights of step j written: its S has taken K of step j - 2, ring tile 2 j - 4, long ago
+        if (!(ok = wait_bar_w(&bar[L::PREADY], (uint32_t)(j & 1), ctl, err) && ring_full<D>(bar, c, ctl, err))) break;
         tc::fence_after_sync();
-        const uint32_t vb = (uint32_t)(c % L::NST) * L::TILE + b * (STEP * 128);
+        const uint32_t vb = (uint32_t)(c % L::NST) * L::KTILE;
 #pragma unroll
         for (int kk = 0; kk < STEP / 16; ++kk)
-            tc::mma_bf16_ts_off_w(tm + L::TM_O + u * D, tm + L::TM_P + u * 32 + 8 * kk, dv, vb + kk * 2048, id_o,
-                                  (j > 0 || kk > 0) ? 1u : 0u);
-        tc::mma_commit_w(&bar[L::PVD + u]);
-        if (b || j + 1 == myns) tc::mma_commit_w(&bar[L::EMPTY + c % L::NST]);
+            tc::mma_bf16_ts_off_w(tm + L::TM_O, tm + L::TM_P + 8 * kk, dv, vb + kk * 2048, id_o, (j > 0 || kk > 0) ? 1u : 0u);
+        tc::mma_commit_w(&bar[L::PVD]);
+        tc::mma_commit_w(&bar[L::EMPTY + c % L::NST]);
     }
 }
 
 template <int D, bool PREFIX>
-__global__ void __launch_bounds__(NTHREADS, 1)
+__global__ void __launch_bounds__(NTHREADS, 2)
     k_attn_prefill(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                    const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ AttnPrefill a) {
     using L = Layout<D>;
-    extern __shared__ uint8_t smem_raw[];
-    const uint32_t raw_base = tc::smem_u32(smem_raw);
-    uint8_t *smem = smem_raw + ((1024u - (raw_base & 1023u)) & 1023u);
+    extern __shared__ __align__(1024) uint8_t smem[];
     const uint32_t sb = tc::smem_u32(smem);
     // (a shuffle, so that the compiler knows the roles' branches to be warp-uniform and keeps the product
     // warps' operands in uniform registers)
@@ -181,14 +165,13 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         it.split = rem - it.head * a.splits;
         it.t0 = 0;
         it.len = a.T_tot;
-        it.pos0 = rb * 2 * P;
+        it.pos0 = rb * P;
         // steps spread over the splits as evenly as they go
         const int steps = (a.prefix_len + STEP - 1) / STEP;
         const int k0 = (int)((int64_t)steps * it.split / a.splits), k1 = (int)((int64_t)steps * (it.split + 1) / a.splits);
         it.k0 = k0 * STEP;
         it.keys = a.prefix_len - it.k0;
-        it.ns0 = k1 - k0;
-        it.ns1 = it.pos0 + P < it.len ? it.ns0 : 0;
+        it.ns = k1 - k0;
     } else {
         // blocks are numbered so that the query tiles with the most key tiles come first
         const int per = a.Hkv * a.N, r = blockIdx.x / per, rem = blockIdx.x - r * per;
@@ -205,21 +188,22 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         int t1;
         seq_bounds(a.cu, n, a.N, a.T_tot, it.t0, t1);
         it.len = t1 - it.t0;
-        it.pos0 = (a.blocks - 1 - r) * 2 * P;
+        it.pos0 = (a.blocks - 1 - r) * P;
         if (it.pos0 >= it.len) return;
         it.k0 = it.t0;
         it.keys = it.len;
-        const int e0 = min(it.pos0 + P, it.len), e1 = min(it.pos0 + 2 * P, it.len);
-        it.ns0 = (e0 + STEP - 1) / STEP;
-        it.ns1 = e1 > it.pos0 + P ? (e1 + STEP - 1) / STEP : 0;
+        it.ns = (min(it.pos0 + P, it.len) + STEP - 1) / STEP;
     }
-    const int ns = max(it.ns0, it.ns1), nk = (ns + 1) / 2;  // steps, ring tiles
+    if (sb & 1023u) {  // the operand tiles' swizzle counts on it
+        if (tid == 0) atomicOr(a.err, ERRBIT_INTERNAL);
+        return;
+    }
 
     uint64_t *bar = reinterpret_cast<uint64_t *>(smem + L::OFF_BAR);
     Ctl *ctl = reinterpret_cast<Ctl *>(smem + L::OFF_CTL);
-    if (warp == W_MMA) tc::tmem_alloc(&ctl->tmem, 512);
+    if (warp == W_S) tc::tmem_alloc(&ctl->tmem, 256);
     if (tid == W_LOAD * 32) {
-        for (int i = 0; i < L::NBAR; ++i) tc::mbar_init(&bar[i], (i >= L::SFREE && i < L::PVD) ? 4u : i == L::FIN ? 4u : (i >= L::EMPTY && i < L::SFULL) ? 2u : 1u);
+        for (int i = 0; i < L::NBAR; ++i) tc::mbar_init(&bar[i], (i >= L::SFREE && i < L::PVD) ? 4u : i == L::FIN ? 2u : 1u);
         ctl->abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -230,21 +214,18 @@ __global__ void __launch_bounds__(NTHREADS, 1)
 
     if (warp == W_LOAD) {
         if (lane == 0) {
-            const uint32_t bytes = (uint32_t)(a.G * P) * 128u * (D / 64);
-            tc::mbar_arrive_expect_tx(&bar[L::QFULL], it.ns1 ? 2 * bytes : bytes);
-            for (int u = 0; u < (it.ns1 ? 2 : 1); ++u)
+            tc::mbar_arrive_expect_tx(&bar[L::QFULL], (uint32_t)(a.G * P) * 128u * (D / 64));
 #pragma unroll
-                for (int hf = 0; hf < D / 64; ++hf)
-                    tc::tma_load_3d(sb + L::OFF_Q + u * L::TILE + hf * 16384, &tm_q, &bar[L::QFULL], 64 * hf, it.head * a.G,
-                                    it.t0 + it.pos0 + u * P);
+            for (int hf = 0; hf < D / 64; ++hf)
+                tc::tma_load_3d(sb + L::OFF_Q + hf * L::QBLOCK, &tm_q, &bar[L::QFULL], 64 * hf, it.head * a.G, it.t0 + it.pos0);
         }
         __syncwarp();
         // paged: lane i brings box i of a tile (a page's rows, 64 of them at most), whose page number it fetched a
         // tile ahead
-        const int box_log = min(a.page_log, 6), boxes = PREFIX ? TK >> box_log : 1, rows = TK / boxes;
+        const int box_log = min(a.page_log, 6), boxes = PREFIX ? STEP >> box_log : 1, rows = STEP / boxes;
         const int npages = PREFIX ? (a.prefix_len + (1 << a.page_log) - 1) >> a.page_log : 0;
         auto page_of = [&](int j) {
-            const int i = (it.k0 + j * TK + (lane << box_log)) >> a.page_log;
+            const int i = (it.k0 + j * STEP + (lane << box_log)) >> a.page_log;
             int p = a.num_pages;  // beyond the tensor: reads as zero
             if (lane < boxes && i < npages) {
                 const int x = a.pages[i];
@@ -255,97 +236,80 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         int page = PREFIX ? page_of(0) : 0;
         bool ok = true;
         int c = 0;  // tiles brought
-        for (int j = 0; ok && j < nk; ++j) {
+        for (int j = 0; ok && j < it.ns; ++j) {
             for (int kv = 0; kv < 2; ++kv, ++c) {
                 const int st = c % L::NST;
                 if (c >= L::NST && !(ok = wait_bar_w(&bar[L::EMPTY + st], (uint32_t)((c / L::NST - 1) & 1), ctl, a.err))) break;
-                if (lane == 0) {
-                    if (2 * j >= it.ns0) tc::mbar_arrive(&bar[L::EMPTY + st]);  // a query tile that does not use it
-                    if (2 * j >= it.ns1) tc::mbar_arrive(&bar[L::EMPTY + st]);
-                    tc::mbar_arrive_expect_tx(&bar[L::FULL + st], L::TILE);
-                }
+                if (lane == 0) tc::mbar_arrive_expect_tx(&bar[L::FULL + st], L::KTILE);
                 __syncwarp();
                 const CUtensorMap *map = kv ? &tm_v : &tm_k;
-                const uint32_t dst = sb + L::OFF_KV + st * L::TILE + lane * rows * 128;
+                const uint32_t dst = sb + L::OFF_KV + st * L::KTILE + lane * rows * 128;
                 if (lane < boxes) {
 #pragma unroll
                     for (int hf = 0; hf < D / 64; ++hf) {
                         if (PREFIX)
-                            tc::tma_load_3d(dst + hf * 16384, map, &bar[L::FULL + st], 64 * hf,
-                                            (it.k0 + j * TK + (lane << box_log)) & ((1 << a.page_log) - 1), page * a.Hkv + it.head);
+                            tc::tma_load_3d(dst + hf * L::KBLOCK, map, &bar[L::FULL + st], 64 * hf,
+                                            (it.k0 + j * STEP + (lane << box_log)) & ((1 << a.page_log) - 1), page * a.Hkv + it.head);
                         else
-                            tc::tma_load_3d(dst + hf * 16384, map, &bar[L::FULL + st], 64 * hf, it.head, it.k0 + j * TK);
+                            tc::tma_load_3d(dst + hf * L::KBLOCK, map, &bar[L::FULL + st], 64 * hf, it.head, it.k0 + j * STEP);
                     }
                 }
             }
-            if (PREFIX && j + 1 < nk) page = page_of(j + 1);
+            if (PREFIX && j + 1 < it.ns) page = page_of(j + 1);
         }
         if (lane == 0) {
             attn::drain_bar(&bar[L::QFULL], 0);
             for (int i = std::max(c - L::NST, 0); i < c; ++i) attn::drain_bar(&bar[L::FULL + i % L::NST], (i / L::NST) & 1);
         }
         __syncwarp();
-    } else if (warp >= W_MMA) {
-        if (warp == W_MMA)
-            s_loop<D>(std::integral_constant<int, 0>(), it.ns0, tm, sb, bar, ctl, a.err);
-        else if (warp == W_MMA + 1)
-            s_loop<D>(std::integral_constant<int, 1>(), it.ns1, tm, sb, bar, ctl, a.err);
-        else if (warp == W_MMA + 2)
-            pv_loop<D>(std::integral_constant<int, 0>(), it.ns0, tm, sb, bar, ctl, a.err);
+    } else if (warp >= W_S) {
+        if (warp == W_S)
+            s_loop<D>(it.ns, tm, sb, bar, ctl, a.err);
         else
-            pv_loop<D>(std::integral_constant<int, 1>(), it.ns1, tm, sb, bar, ctl, a.err);
+            o_loop<D>(it.ns, tm, sb, bar, ctl, a.err);
         // tensor memory may go once every product is done
         tc::mma_commit_w(&bar[L::FIN]);
         if (lane == 0) attn::drain_bar(&bar[L::FIN], 0);
         __syncwarp();
     } else {
         // ---------------------------------------------------------------- softmax (one query row per thread)
-        const int u = warp >> 2, r = tid & 127;
+        const int r = tid;
         const uint32_t tl = tm + ((uint32_t)((warp & 3) * 32) << 16);
-        const uint32_t to = tl + L::TM_O + u * D;
-        const int myns = u ? it.ns1 : it.ns0;
-        const int pos = it.pos0 + u * P + r / a.G;  // position within the sequence
-        const int first = it.pos0 + u * P;          // the tile's first position
+        const uint32_t to = tl + L::TM_O;
+        const int pos = it.pos0 + r / a.G;  // position within the sequence
         const float sc = a.scale_log2;
         float m_ref = -INFINITY, l = 0.f;
         bool ok = true;
-        if (u < L::QT_TILES && myns) {
-            // this row of Q to tensor memory, where the products for S read it without shared memory
-            ok = wait_bar_w(&bar[L::QFULL], 0, ctl, a.err);
-            if (ok) {
+        // this row's first 64 columns of Q to tensor memory
+        if ((ok = wait_bar_w(&bar[L::QFULL], 0, ctl, a.err))) {
+            uint32_t w[32];
 #pragma unroll
-                for (int hf = 0; hf < D / 64; ++hf) {
-                    uint32_t w[32];
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const uint4 x = *reinterpret_cast<const uint4 *>(smem + L::OFF_Q + u * L::TILE + hf * 16384 + r * 128 + ((i ^ (r & 7)) << 4));
-                        w[4 * i] = x.x;
-                        w[4 * i + 1] = x.y;
-                        w[4 * i + 2] = x.z;
-                        w[4 * i + 3] = x.w;
-                    }
-                    tc::tmem_st32(tl + L::TM_Q + u * (D / 2) + hf * 32, w);
-                }
-                tc::tmem_st_wait();
-                tc::fence_before_sync();
-                __syncwarp();
-                if (lane == 0) tc::mbar_arrive(&bar[L::QT + u]);
+            for (int i = 0; i < 8; ++i) {
+                const uint4 x = *reinterpret_cast<const uint4 *>(smem + L::OFF_Q + r * 128 + ((i ^ (r & 7)) << 4));
+                w[4 * i] = x.x;
+                w[4 * i + 1] = x.y;
+                w[4 * i + 2] = x.z;
+                w[4 * i + 3] = x.w;
             }
+            tc::tmem_st32(tl + L::TM_Q, w);
+            tc::tmem_st_wait();
+            tc::fence_before_sync();
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(&bar[L::QT]);
         }
-        for (int j = 0; ok && j < myns; ++j) {
-            const uint32_t ts = tl + L::TM_S + u * 64;
-            if (!(ok = wait_bar_w(&bar[L::SFULL + u], (uint32_t)(j & 1), ctl, a.err))) break;
+        for (int j = 0; ok && j < it.ns; ++j) {
+            if (!(ok = wait_bar_w(&bar[L::SFULL], (uint32_t)(j & 1), ctl, a.err))) break;
             tc::fence_after_sync();
-            // keys beyond this row's position, or beyond the prefix, are masked
             uint32_t s[2][32];
-            attn::tmem_ld32x(ts, s[0]);
-            attn::tmem_ld32x(ts + 32, s[1]);
+            attn::tmem_ld32x(tl + L::TM_S, s[0]);
+            attn::tmem_ld32x(tl + L::TM_S + 32, s[1]);
             tc::tmem_wait_ld(s[0]);
             tc::tmem_wait_ld(s[1]);
             tc::fence_before_sync();
             __syncwarp();
-            if (lane == 0) tc::mbar_arrive(&bar[L::SFREE + u]);  // the next S may overwrite these
-            if (PREFIX ? it.keys - j * STEP < STEP : first - j * STEP < STEP - 1) {
+            if (lane == 0) tc::mbar_arrive(&bar[L::SFREE]);  // the next S may overwrite these
+            // keys beyond this row's position, or beyond the prefix, are masked
+            if (PREFIX ? it.keys - j * STEP < STEP : it.pos0 - j * STEP < STEP - 1) {
                 const int lim = (PREFIX ? it.keys - 1 : pos) - j * STEP;
 #pragma unroll
                 for (int i = 0; i < STEP; ++i)
@@ -368,7 +332,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                 l *= alpha;
             }
             if (j > 0 && __any_sync(0xffffffffu, grow)) {
-                if (!(ok = wait_bar_w(&bar[L::PVD + u], (uint32_t)((j - 1) & 1), ctl, a.err))) break;
+                if (!(ok = wait_bar_w(&bar[L::PVD], (uint32_t)((j - 1) & 1), ctl, a.err))) break;
                 tc::fence_after_sync();
 #pragma unroll 1
                 for (int c0 = 0; c0 < D; c0 += 32) {
@@ -380,8 +344,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                     tc::tmem_st32(to + c0, w);
                 }
             }
-            // the weights as bf16 pairs over the first 32 columns of the buffer. For D = 64, where the products take
-            // half the time, the MUFU (8 cycles a warp's exponential) would be the bound, and the FMA pipe takes a quarter
+            // the weights as bf16 pairs
             uint64_t ps[2] = {0, 0};
             const uint64_t sc2 = attn::pack2(sc, sc), mm2 = attn::pack2(-m_ref, -m_ref);
             uint32_t w[32];
@@ -389,49 +352,41 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             for (int i = 0; i < 32; ++i) {
                 const uint64_t x = attn::fma2(attn::pack2(S(2 * i), S(2 * i + 1)), sc2, mm2);
                 float p0, p1;
-                if ((i & 3) >= 4 - L::POLY / 2) {
-                    attn::exp2_poly(x, p0, p1);
-                } else {
-                    attn::unpack2(x, p0, p1);
-                    p0 = chunk::ex2(p0);
-                    p1 = chunk::ex2(p1);
-                }
+                attn::unpack2(x, p0, p1);
+                p0 = chunk::ex2(p0);
+                p1 = chunk::ex2(p1);
                 ps[i & 1] = attn::add2(ps[i & 1], attn::pack2(p0, p1));
                 w[i] = tc::pack_bf16x2(p0, p1);
             }
             if (j >= 1) {  // the last weights have been read
-                if (!(ok = wait_bar_w(&bar[L::PVD + u], (uint32_t)((j - 1) & 1), ctl, a.err))) break;
+                if (!(ok = wait_bar_w(&bar[L::PVD], (uint32_t)((j - 1) & 1), ctl, a.err))) break;
                 tc::fence_after_sync();
             }
-            tc::tmem_st32(tl + L::TM_P + u * 32, w);
+            tc::tmem_st32(tl + L::TM_P, w);
             float a0, a1;
             attn::unpack2(attn::add2(ps[0], ps[1]), a0, a1);
             l += a0 + a1;
             if (it.keys - j * STEP < STEP) {
                 // rows of V beyond the sequence or the prefix: another sequence's values or stale slots
-                const int c = j | 1, st = c % L::NST, n = it.keys - j * STEP;
+                const int c = 2 * j + 1, st = c % L::NST, n = it.keys - j * STEP;
                 if (!(ok = wait_bar_w(&bar[L::FULL + st], (uint32_t)((c / L::NST) & 1), ctl, a.err))) break;
                 if (r >= n && r < STEP) {
 #pragma unroll
                     for (int hf = 0; hf < D / 64; ++hf)
 #pragma unroll
                         for (int i = 0; i < 8; ++i)
-                            chunk::st_shared_v4(sb + L::OFF_KV + st * L::TILE + hf * 16384 + ((j & 1) * STEP + r) * 128 + i * 16, 0, 0,
-                                                0, 0);
+                            chunk::st_shared_v4(sb + L::OFF_KV + st * L::KTILE + hf * L::KBLOCK + r * 128 + i * 16, 0, 0, 0, 0);
                 }
                 tc::fence_smem_to_async();
             }
             tc::tmem_st_wait();
             tc::fence_before_sync();
             __syncwarp();
-            if (lane == 0) {
-                tc::mbar_arrive(&bar[L::PREADY + u]);
-                if (u == 0 && j == 0) tc::mbar_arrive(&bar[L::START]);  // (PREADY's phases come round; this one's does not)
-            }
+            if (lane == 0) tc::mbar_arrive(&bar[L::PREADY]);
         }
-        if (ok && myns)
-            ok = wait_bar_w(&bar[L::PVD + u], (uint32_t)((myns - 1) & 1), ctl, a.err);
-        if (ok && myns) {
+        if (ok)
+            ok = wait_bar_w(&bar[L::PVD], (uint32_t)((it.ns - 1) & 1), ctl, a.err);
+        if (ok) {
             tc::fence_after_sync();
             const bool valid = r < a.G * P && pos < it.len;
             const int64_t row = (int64_t)(it.t0 + pos) * a.Hq + it.head * a.G + r % a.G;
@@ -468,19 +423,19 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     }
     tc::fence_before_sync();
     __syncthreads();
-    if (warp == W_MMA) tc::tmem_dealloc(tm, 512);
+    if (warp == W_S) tc::tmem_dealloc(tm, 256);
 }
 
 template <int D>
 cudaError_t launch_prompt(AttnPrefill a, cudaStream_t st, const char **stage) {
     cudaError_t e;
     a.P = TQ / a.G;
-    a.blocks = (a.max_len + 2 * a.P - 1) / (2 * a.P);
+    a.blocks = (a.max_len + a.P - 1) / a.P;
     CUtensorMap tm_q, tm_k, tm_v;
     *stage = "TMA descriptor encoding";
     if ((e = attn::make_map(&tm_q, a.q, D, a.Hq, a.T_tot, D, a.q_stride, a.G, a.P)) != cudaSuccess) return e;
-    if ((e = attn::make_map(&tm_k, a.k, D, a.Hkv, a.T_tot, D, a.k_stride, 1, TK)) != cudaSuccess) return e;
-    if ((e = attn::make_map(&tm_v, a.v, D, a.Hkv, a.T_tot, D, a.v_stride, 1, TK)) != cudaSuccess) return e;
+    if ((e = attn::make_map(&tm_k, a.k, D, a.Hkv, a.T_tot, D, a.k_stride, 1, STEP)) != cudaSuccess) return e;
+    if ((e = attn::make_map(&tm_v, a.v, D, a.Hkv, a.T_tot, D, a.v_stride, 1, STEP)) != cudaSuccess) return e;
     *stage = "attn_prefill";
     auto kern = k_attn_prefill<D, false>;
     if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Layout<D>::SMEM)) != cudaSuccess)
@@ -495,7 +450,7 @@ template <int D>
 cudaError_t launch_prefix(AttnPrefill a, cudaStream_t st, const char **stage) {
     cudaError_t e;
     a.P = TQ / a.G;
-    a.blocks = (a.T_tot + 2 * a.P - 1) / (2 * a.P);
+    a.blocks = (a.T_tot + a.P - 1) / a.P;
     CUtensorMap tm_q, tm_k, tm_v;
     *stage = "TMA descriptor encoding";
     const uint64_t page = 1u << a.page_log, n = (uint64_t)a.num_pages * a.Hkv;

@@ -104,6 +104,7 @@ cudaError_t launch_attn_prefix(const AttnPrefill &a, int d, cudaStream_t st, con
 
 // Attention of one token per sequence over the paged cache (see gdn_attn_decode).
 constexpr int kDecodeCtas = 148;  // runs that the own keys are cut into: one per SM
+constexpr int kPrefixCtas = 296;  // CTAs of the prefix kernel: two per SM
 struct AttnDecode {
     const __nv_bfloat16 *q, *k_cache, *v_cache;
     const int32_t *table, *lens;  // [B][max_pages], [B]
