@@ -12,8 +12,15 @@ without the library)::
     chunk_fwd(q, k, v, g, beta, S0=None, cu_seqlens=None, o=None, S_T=None) -> (o, S_T)
     decode_step(q, k, v, g, beta, S, o=None) -> o           # S updated in place
     seq_scan(q, k, v, g, beta, S0=None, cu_seqlens=None) -> (o, S_T)
+
+and the backbone's attention layers in serving::
+
+    qk_norm_rope(q, k, wq, wk, positions, v=None, k_cache=None, v_cache=None, slots=None) -> (q, k)
+    attn_prefill(q, k, v, cu_seqlens=None, max_len=None) -> o
+    attn_decode(q, k_cache, v_cache, page_table, lens, prefix_pages=None, prefix_len=0) -> o
 """
-_EXPORTS = ("chunk_fwd", "decode_step", "seq_scan", "chunk_fwd_workspace_size", "library_path",
+_EXPORTS = ("chunk_fwd", "decode_step", "seq_scan", "qk_norm_rope", "attn_prefill", "attn_decode",
+            "chunk_fwd_workspace_size", "library_path",
             "GdnError", "load_library")
 
 

@@ -496,7 +496,7 @@ gdn_status gdn_attn_prefill(const void *q, int64_t q_stride, const void *k, int6
     if (!stride_ok(q_stride, T_tot, Hq, d, 2) || !stride_ok(k_stride, T_tot, Hkv, d, 2) ||
         !stride_ok(v_stride, T_tot, Hkv, d, 2))
         return fail(GDN_ERR_SHAPE, "token strides must cover a token's heads and be multiples of 16 bytes");
-    // TMA strides are below 2^40 bytes; the grid has a block per query tile pair, key head and sequence
+    // TMA strides are below 2^40 bytes; the grid has a block per query tile, key head and sequence
     const int64_t pos = 128 / (Hq / Hkv);
     if (std::max({q_stride, k_stride, v_stride}) >= ((int64_t)1 << 39) ||
         (double)((max_len + pos - 1) / pos) * Hkv * N >= 2.0e9)

@@ -95,7 +95,7 @@ struct AttnPrefill {
     int num_pages, page_log, prefix_len, splits;
     float *part_o;    // [splits][B][Hq][d] unnormalised
     float2 *part_ml;  // [splits][B][Hq] reference maximum (log2 units) and sum
-    int P, blocks;    // set by the launcher: positions per query tile, query tile pairs of the longest sequence
+    int P, blocks;    // set by the launcher: positions per query tile, query tiles of the longest sequence
 };
 cudaError_t launch_attn_prefill(const AttnPrefill &a, int d, cudaStream_t st, const char **stage);
 

@@ -22,9 +22,10 @@
 // is: with few tokens (a decode step) each warp has one group of rows; with many a warp walks through
 // tokens, computes a token's sines and cosines once for all of its heads there (a lane keeps the same
 // columns for every row), loads the next rows while it works on these and asks L2 for those a token on.
-// 10240 tokens, 16 + 4 heads of 128 in bf16, keys and values cached: 136 MB in 29.5 us (4.6 TB/s; a plain
-// copy of as many bytes takes 23.4 us). One run a lane with shuffled partners, a token a warp: 40 us; without
-// the L2 prefetch: 33 us; 3 CTAs per SM: 30.1 us, 5 (two row groups no longer fit the registers): 32.7 us.
+// 10240 tokens, 16 + 4 heads of 128 in bf16, keys and values cached: 136 MB in 28.1 us (4.85 TB/s; a plain
+// copy of as many bytes takes 23.4 us), issue slots 58 % busy. One run a lane with shuffled partners, a token a
+// warp: 40 us; at 29.5 us, without the L2 prefetch 33; with 3 CTAs per SM 30.1, with 5 (two row groups no longer
+// fit the registers) 32.7. A decode step's 64 tokens: 2.7 us, a launch.
 #include <math.h>
 
 #include <algorithm>
