@@ -512,7 +512,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // One CTA per (sequence, query head): joins the pieces of its own keys with those of the prefix. A row
 // that the decode kernel finished is left alone; one without any keys is zero.
-constexpr int kMostPieces = kDecodeCtas + kPrefixCtas;  // a piece per CTA and per split of the prefix at most
+constexpr int kMostPieces = kDecodeCtas + kPromptCtas;  // a piece per CTA and per split of the prefix at most
 template <int D>
 __global__ void __launch_bounds__(128) k_attn_combine(const __grid_constant__ AttnDecode a) {
     constexpr int LPR = D / 4, SUBS = 128 / LPR, AHEAD = 4;  // lanes per row; pieces read together; and ahead
@@ -674,7 +674,7 @@ int attn_decode_splits(int B, int Hq, int Hkv, int prefix_len) {
     // as many splits of the prefix's steps of 64 keys as the GPU holds at once
     const int64_t pos = 128 / (Hq / Hkv), blocks = (B + pos - 1) / pos * Hkv;
     const int64_t steps = ((int64_t)prefix_len + 63) / 64;
-    return (int)std::max<int64_t>(1, std::min<int64_t>(steps, kPrefixCtas / blocks));
+    return (int)std::max<int64_t>(1, std::min<int64_t>(steps, kPromptCtas / blocks));
 }
 
 size_t attn_decode_slots(int B, int Hq, int Hkv, int prefix_len) {

@@ -499,7 +499,7 @@ gdn_status gdn_attn_prefill(const void *q, int64_t q_stride, const void *k, int6
     // TMA strides are below 2^40 bytes; the grid has a block per query tile, key head and sequence
     const int64_t pos = 128 / (Hq / Hkv);
     if (std::max({q_stride, k_stride, v_stride}) >= ((int64_t)1 << 39) ||
-        (double)((max_len + pos - 1) / pos) * Hkv * N >= 2.0e9)
+        (double)std::min((max_len + pos - 1) / pos * N, gdn::attn_prefill_tiles(T_tot, N, (int)pos)) * Hkv >= 5.0e8)
         return fail(GDN_ERR_SHAPE, "sizes overflow");
     if (T_tot > 0 && (!q || !k || !v || !o)) return fail(GDN_ERR_NULL, "q, k, v and o are required");
     const void *ptrs[] = {q, k, v, o};
@@ -517,9 +517,9 @@ gdn_status gdn_attn_prefill(const void *q, int64_t q_stride, const void *k, int6
     a.q = static_cast<const __nv_bfloat16 *>(q);
     a.k = static_cast<const __nv_bfloat16 *>(k);
     a.v = static_cast<const __nv_bfloat16 *>(v);
-    a.q_stride = q_stride;
-    a.k_stride = k_stride;
-    a.v_stride = v_stride;
+    a.q_stride = T_tot > 1 ? q_stride : (int64_t)Hq * d;  // (of one token any is good)
+    a.k_stride = T_tot > 1 ? k_stride : (int64_t)Hkv * d;
+    a.v_stride = T_tot > 1 ? v_stride : (int64_t)Hkv * d;
     a.cu = cu_seqlens;
     a.N = N;
     a.T_tot = T_tot;

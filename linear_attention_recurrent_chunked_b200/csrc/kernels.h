@@ -82,6 +82,7 @@ cudaError_t launch_norm_rope(const NormRope &a, int d, bool bf16, cudaStream_t s
 // Causal attention with grouped heads over packed prompts (see gdn_attn_prefill), and the part of
 // gdn_attn_decode over the prefix that a batch shares. The fields after `err` are the latter's; for it
 // q is [B][Hq][d] with T_tot = B, and k, v are the cache.
+constexpr int kPromptCtas = 296;  // CTAs that the GPU holds at once: two per SM
 struct AttnPrefill {
     const __nv_bfloat16 *q, *k, *v;
     int64_t q_stride, k_stride, v_stride;  // elements from one token to the next
@@ -96,7 +97,9 @@ struct AttnPrefill {
     float *part_o;    // [splits][B][Hq][d] unnormalised
     float2 *part_ml;  // [splits][B][Hq] reference maximum (log2 units) and sum
     int P, blocks;    // set by the launcher: positions per query tile, query tiles of the longest sequence
+    bool dense;       // also: blocks numbered sequence by sequence
 };
+int64_t attn_prefill_tiles(int T_tot, int N, int P);  // most query tiles that N sequences of T_tot tokens can have
 cudaError_t launch_attn_prefill(const AttnPrefill &a, int d, cudaStream_t st, const char **stage);
 
 // The same kernel without the mask over a cached prefix that a batch shares: partial results per split.
@@ -104,7 +107,6 @@ cudaError_t launch_attn_prefix(const AttnPrefill &a, int d, cudaStream_t st, con
 
 // Attention of one token per sequence over the paged cache (see gdn_attn_decode).
 constexpr int kDecodeCtas = 148;  // runs that the own keys are cut into: one per SM
-constexpr int kPrefixCtas = 296;  // CTAs of the prefix kernel: two per SM
 struct AttnDecode {
     const __nv_bfloat16 *q, *k_cache, *v_cache;
     const int32_t *table, *lens;  // [B][max_pages], [B]

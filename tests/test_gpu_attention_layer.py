@@ -204,6 +204,50 @@ def test_prefill_many_sequences(N):
     close(o, ref, attn_tol(ref, a, q, k, 64, 400))
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("where", [0, 150, 299])
+def test_prefill_one_long_prompt_among_many_short(where, d):
+    """One prompt that is far longer than the others, first, among or last of them, empty ones on both sides:
+    every prompt has the bits of a call of its own, and a malformed pack of this kind is not written."""
+    gen = torch.Generator().manual_seed(15 + where)
+    lens = torch.randint(0, 20, (300,), generator=gen).tolist()
+    lens[1] = lens[298] = 0
+    lens[where] = 2500
+    q, k, v, cu = (x.cuda() for x in prompt(gen, lens, 8, 2, d))
+    v = v[:, 8 + 2:]
+    o = gdn.attn_prefill(q, k, v, cu, max_len=2500, check=True)
+    ends = np.cumsum(lens)
+    for n in (0, 2, where, 149, 151, 297, 299):
+        i, j = ends[n] - lens[n], ends[n]
+        if i < j:
+            assert torch.equal(o[i:j], gdn.attn_prefill(q[i:j], k[i:j], v[i:j], check=True))
+    i = ends[where] - 40
+    ref, a = al.prompt_attention(q[ends[where] - 2500:ends[where]], k[ends[where] - 2500:ends[where]],
+                                 v[ends[where] - 2500:ends[where]], [2500])
+    close(o[i:i + 40], ref[-40:], attn_tol(ref, a, q, k, d, 2500)[-40:])
+    for at, value in ((0, 1), (300, int(ends[-1]) - 1), (where + 1, int(ends[where]) + 1), (77, -5)):
+        bad = cu.clone()
+        bad[at] = value
+        kept = torch.full_like(o, 3.0)
+        with pytest.raises(gdn.GdnError) as e:
+            gdn.attn_prefill(q, k, v, bad, max_len=2500, o=kept, check=True)
+        assert e.value.status == 5 and (kept == 3.0).all()
+
+
+def test_prefill_one_token_with_any_stride():
+    """Of a single token the distance to the next one is not looked at."""
+    gen = torch.Generator().manual_seed(16)
+    q, k, v, _ = (x.cuda() for x in prompt(gen, [1], 4, 2, 64))
+    o, ws = torch.zeros_like(q), torch.zeros(256, dtype=torch.uint8, device="cuda")
+    v = v[:, 6:].contiguous()
+    for stride in (0, 8, 1 << 30):
+        o.zero_()
+        gdn._check(gdn.load_library().gdn_attn_prefill(
+            q.data_ptr(), stride, k.data_ptr(), stride, v.data_ptr(), stride, None, 1, 1, 4, 2, 64, 1, 0.0, gdn.GDN_BF16,
+            o.data_ptr(), ws.data_ptr(), 256, torch.cuda.current_stream().cuda_stream))
+        assert torch.equal(o, v.repeat_interleave(2, 1))
+
+
 @pytest.mark.parametrize("trend", ["rising", "falling", "spikes"])
 @pytest.mark.parametrize("d", [64, 128])
 def test_prefill_moving_maximum(trend, d):
