@@ -26,7 +26,7 @@
 // k_attn_combine joins the pieces; it is launched to start while the kernel before it drains.
 //
 // 64 sequences of 512 to 10,240 keys, 16/4 heads, d = 128 (427 MB): 76 us with the combine kernel, 5.6 TB/s. Three
-// sequences of 10,240 to 40,960, 16/2 heads (61 MB): 21 us. One of 2,048: 8.8 us, of which 4.8 remain with no key
+// sequences of 10,240 to 40,960, 16/2 heads (61 MB): 20 us. One of 2,048: 8.5 us, of which 4.8 remain with no key
 // at all (two launches, the lengths). 64 sequences behind a prefix of 10,230: 27 us, of which the prefix 15: 37 splits
 // of it fill two CTAs per SM with 4 or 5 steps of 64 keys each, whose results are 19 MB (half the splits, twice
 // the steps: 27 us too).
@@ -510,13 +510,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (a.prefix_len) grid_wait();  // this kernel's end then means the prefix kernel's too
 }
 
-// One CTA per (sequence, query head): joins the pieces of its own keys with those of the prefix. A row
-// that the decode kernel finished is left alone; one without any keys is zero.
+// One CTA per sequence and a.rows of its query heads: joins each one's pieces of its own keys with those of the
+// prefix. A row that the decode kernel finished is left alone; one without any keys is zero.
 constexpr int kMostPieces = kDecodeCtas + kPromptCtas;  // a piece per CTA and per split of the prefix at most
+constexpr int kCombineCtas = 148 * 9;  // that run at once, by registers
 template <int D>
 __global__ void __launch_bounds__(128) k_attn_combine(const __grid_constant__ AttnDecode a) {
     constexpr int LPR = D / 4, SUBS = 128 / LPR, AHEAD = 4;  // lanes per row; pieces read together; and ahead
-    const int row = blockIdx.x, b = row / a.Hq, hq = row - b * a.Hq, h = hq / a.G, g = hq - h * a.G;
+    const int per = (a.Hq + a.rows - 1) / a.rows, b = blockIdx.x / per, hq0 = (blockIdx.x - b * per) * a.rows;
     const int tid = threadIdx.x, sub = tid / LPR, d = tid % LPR * 4;
     __shared__ int sums[2][4];
     __shared__ float weight[kMostPieces], red[2][4];
@@ -535,19 +536,26 @@ __global__ void __launch_bounds__(128) k_attn_combine(const __grid_constant__ At
         sums[1][tid >> 5] = total;
     }
     bool bad = false;
-    if (row == 0) {
+    if (blockIdx.x == 0) {
         const int np = (int)(((int64_t)a.prefix_len + (1 << a.page_log) - 1) >> a.page_log);
         for (int i = tid; i < np; i += 128) bad |= a.prefix_pages[i] < 0 || a.prefix_pages[i] >= a.num_pages;
     }
     __syncthreads();
     const int steps = (sums[1][0] + sums[1][1] + sums[1][2] + sums[1][3]) * a.Hkv;
-    const int x0 = (sums[0][0] + sums[0][1] + sums[0][2] + sums[0][3]) * a.Hkv + h * n;
-    int c0 = 0, own = 0;  // first CTA with a piece, number of pieces
-    if (n) {
-        c0 = cta_of(steps, x0);
-        own = cta_of(steps, x0 + n - 1) - c0 + 1;
-    }
-    const int all = own + (a.prefix_len ? a.splits : 0);
+    const int x_seq = (sums[0][0] + sums[0][1] + sums[0][2] + sums[0][3]) * a.Hkv;
+    int row, h, g, c0, own, all;  // the row, the first CTA with a piece of it, its own pieces and all
+    auto set_row = [&](int hq) {
+        row = b * a.Hq + hq;
+        h = hq / a.G;
+        g = hq - h * a.G;
+        c0 = own = 0;
+        if (n) {
+            c0 = cta_of(steps, x_seq + h * n);
+            own = cta_of(steps, x_seq + h * n + n - 1) - c0 + 1;
+        }
+        all = own + (a.prefix_len ? a.splits : 0);
+    };
+    set_row(hq0);
     // piece i: a row of the slots, or of the prefix kernel's results
     auto place = [&](int i, const float *&po, const float2 *&ml) {
         const bool mine = i < own;
@@ -559,7 +567,7 @@ __global__ void __launch_bounds__(128) k_attn_combine(const __grid_constant__ At
     };
 
     grid_wait();  // also where nothing is left to do: this kernel's end means the one before it has ended
-    if (row == 0) {
+    if (blockIdx.x == 0) {
         // the error word, from what the decode kernel's CTAs found (the prefix kernel has set it up already)
         uint32_t found = bad ? ERRBIT_PAGES : 0u;
         for (int i = tid; i < kDecodeCtas; i += 128) found |= a.bad[i];
@@ -570,78 +578,86 @@ __global__ void __launch_bounds__(128) k_attn_combine(const __grid_constant__ At
             *a.err = (a.prefix_len ? *a.err : 0u) | (pages ? ERRBIT_PAGES : 0u) | (late ? ERRBIT_TIMEOUT : 0u) |
                      (internal ? ERRBIT_INTERNAL : 0u);
     }
-    if (own == 1 && !a.prefix_len) return;
-
-    // the first pieces set out while the weights are worked out
-    float4 y[AHEAD];
-    const float *po;
-    const float2 *pml;
-    auto fetch = [&](int i0) {
+    for (int hq = hq0;;) {
+        const bool pieces = own != 1 || a.prefix_len;
+        if (pieces) {
+            // the first pieces set out while the weights are worked out
+            float4 y[AHEAD];
+            const float *po;
+            const float2 *pml;
+            auto fetch = [&](int i0) {
 #pragma unroll
-        for (int k = 0; k < AHEAD; ++k) {
-            const int i = i0 + k * SUBS;
-            y[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (i < all) {
-                place(i, po, pml);
-                y[k] = *reinterpret_cast<const float4 *>(po);
+                for (int k = 0; k < AHEAD; ++k) {
+                    const int i = i0 + k * SUBS;
+                    y[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (i < all) {
+                        place(i, po, pml);
+                        y[k] = *reinterpret_cast<const float4 *>(po);
+                    }
+                }
+            };
+            fetch(sub);
+            float2 ml[(kMostPieces + 127) / 128];
+            float top = -INFINITY;
+#pragma unroll
+            for (int k = 0; k < (kMostPieces + 127) / 128; ++k) {
+                ml[k] = make_float2(-INFINITY, 0.f);
+                if (k * 128 + tid < all) {
+                    place(k * 128 + tid, po, pml);
+                    ml[k] = *pml;
+                }
+                top = fmaxf(top, ml[k].x);
+            }
+#pragma unroll
+            for (int i = 16; i; i >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, i));
+            if ((tid & 31) == 0) red[0][tid >> 5] = top;
+            __syncthreads();
+            top = fmaxf(fmaxf(red[0][0], red[0][1]), fmaxf(red[0][2], red[0][3]));
+            float sum = 0.f;
+#pragma unroll
+            for (int k = 0; k < (kMostPieces + 127) / 128; ++k) {
+                const float f = ml[k].x == -INFINITY ? 0.f : exp2f(ml[k].x - top);
+                if (k * 128 + tid < all) weight[k * 128 + tid] = f;
+                sum += f * ml[k].y;
+            }
+#pragma unroll
+            for (int i = 16; i; i >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, i);
+            if ((tid & 31) == 0) red[1][tid >> 5] = sum;
+            __syncthreads();
+            sum = (red[1][0] + red[1][1]) + (red[1][2] + red[1][3]);
+            float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int i0 = sub; i0 < all; i0 += AHEAD * SUBS) {
+#pragma unroll
+                for (int k = 0; k < AHEAD; ++k) {
+                    const float f = i0 + k * SUBS < all ? weight[i0 + k * SUBS] : 0.f;
+                    x.x += f * y[k].x;
+                    x.y += f * y[k].y;
+                    x.z += f * y[k].z;
+                    x.w += f * y[k].w;
+                }
+                if (i0 + AHEAD * SUBS < all) fetch(i0 + AHEAD * SUBS);
+            }
+            part[sub][tid % LPR] = x;
+            __syncthreads();
+            if (!sub) {
+#pragma unroll
+                for (int i = 1; i < SUBS; ++i) {
+                    const float4 z = part[i][tid % LPR];
+                    x.x += z.x;
+                    x.y += z.y;
+                    x.z += z.z;
+                    x.w += z.w;
+                }
+                const float inv = all ? 1.f / sum : 0.f;
+                *reinterpret_cast<uint2 *>(a.o + (int64_t)row * D + d) =
+                    make_uint2(tc::pack_bf16x2(x.x * inv, x.y * inv), tc::pack_bf16x2(x.z * inv, x.w * inv));
             }
         }
-    };
-    fetch(sub);
-    float2 ml[(kMostPieces + 127) / 128];
-    float top = -INFINITY;
-#pragma unroll
-    for (int k = 0; k < (kMostPieces + 127) / 128; ++k) {
-        ml[k] = make_float2(-INFINITY, 0.f);
-        if (k * 128 + tid < all) {
-            place(k * 128 + tid, po, pml);
-            ml[k] = *pml;
-        }
-        top = fmaxf(top, ml[k].x);
+        hq = pieces ? hq + 1 : (h + 1) * a.G;  // (whole for one query head of a group is whole for all)
+        if (hq >= min(hq0 + a.rows, a.Hq)) break;
+        if (pieces) __syncthreads();  // the row's shared values have been read
+        set_row(hq);
     }
-#pragma unroll
-    for (int i = 16; i; i >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, i));
-    if ((tid & 31) == 0) red[0][tid >> 5] = top;
-    __syncthreads();
-    top = fmaxf(fmaxf(red[0][0], red[0][1]), fmaxf(red[0][2], red[0][3]));
-    float sum = 0.f;
-#pragma unroll
-    for (int k = 0; k < (kMostPieces + 127) / 128; ++k) {
-        const float f = ml[k].x == -INFINITY ? 0.f : exp2f(ml[k].x - top);
-        if (k * 128 + tid < all) weight[k * 128 + tid] = f;
-        sum += f * ml[k].y;
-    }
-#pragma unroll
-    for (int i = 16; i; i >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, i);
-    if ((tid & 31) == 0) red[1][tid >> 5] = sum;
-    __syncthreads();
-    sum = (red[1][0] + red[1][1]) + (red[1][2] + red[1][3]);
-    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int i0 = sub; i0 < all; i0 += AHEAD * SUBS) {
-#pragma unroll
-        for (int k = 0; k < AHEAD; ++k) {
-            const float f = i0 + k * SUBS < all ? weight[i0 + k * SUBS] : 0.f;
-            x.x += f * y[k].x;
-            x.y += f * y[k].y;
-            x.z += f * y[k].z;
-            x.w += f * y[k].w;
-        }
-        if (i0 + AHEAD * SUBS < all) fetch(i0 + AHEAD * SUBS);
-    }
-    part[sub][tid % LPR] = x;
-    __syncthreads();
-    if (sub) return;
-#pragma unroll
-    for (int i = 1; i < SUBS; ++i) {
-        const float4 z = part[i][tid % LPR];
-        x.x += z.x;
-        x.y += z.y;
-        x.z += z.z;
-        x.w += z.w;
-    }
-    const float inv = all ? 1.f / sum : 0.f;
-    *reinterpret_cast<uint2 *>(a.o + (int64_t)row * D + d) =
-        make_uint2(tc::pack_bf16x2(x.x * inv, x.y * inv), tc::pack_bf16x2(x.z * inv, x.w * inv));
 }
 
 template <int D, int NT>
@@ -662,7 +678,10 @@ cudaError_t launch(AttnDecode a, cudaStream_t st, const char **stage) {
     if (e != cudaSuccess) return e;
     *stage = "attn_combine";
     pr = prof_start("attn_combine", st);
-    e = attn::launch_early(k_attn_combine<D>, (unsigned)((int64_t)a.B * a.Hq), 128, 0, st, a);
+    // One row per CTA while all of those run at once; beyond, several, since each CTA reads all of the lengths. With one
+    // row for each CTA 4,096 sequences of 100 keys and 16 heads take 353 us and not 192, 1,600 of 500 keys 316 and not 283.
+    a.rows = (int)std::min<int64_t>(a.Hq, ((int64_t)a.B * a.Hq + kCombineCtas - 1) / kCombineCtas);
+    e = attn::launch_early(k_attn_combine<D>, (unsigned)(a.B * ((a.Hq + a.rows - 1) / a.rows)), 128, 0, st, a);
     prof_stop(pr);
     return e;
 }

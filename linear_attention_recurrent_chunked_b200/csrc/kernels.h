@@ -121,6 +121,7 @@ struct AttnDecode {
     float *part_o;  // the prefix kernel's, per split
     float2 *part_ml;
     uint32_t *bad;  // [kDecodeCtas] the error bits of each CTA
+    int rows;       // set by the launcher: query heads that a CTA of the combine kernel takes
 };
 int attn_decode_splits(int B, int Hq, int Hkv, int prefix_len);
 size_t attn_decode_slots(int B, int Hq, int Hkv, int prefix_len);  // rows of d floats

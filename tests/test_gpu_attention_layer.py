@@ -409,6 +409,16 @@ def test_decode_many_sequences_split_anywhere():
     check_decode(cached(gen, lens, 2, 1, 64, 32))
 
 
+@pytest.mark.parametrize("Hq,Hkv,B,prefix", [(14, 2, 700, 0), (13, 1, 350, 40), (13, 13, 350, 0), (16, 1, 500, 100), (6, 2, 500, 0)])
+def test_decode_more_rows_than_run_at_once(Hq, Hkv, B, prefix):
+    """Several query heads for each CTA that joins pieces, in numbers that do not divide the heads, whole and cut
+    sequences, some without keys."""
+    gen = torch.Generator().manual_seed(23 + B + Hq)
+    lens = torch.randint(0, 70, (B,), generator=gen).tolist()
+    lens[B // 3], lens[-1] = 900, 0
+    check_decode(cached(gen, lens, Hq, Hkv, 64, 16, prefix))
+
+
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("Hq,Hkv,page,prefix", [(4, 4, 16, 1), (16, 4, 16, 1000), (16, 4, 64, 2048), (5, 1, 32, 129), (16, 1, 128, 700),
                                                 (6, 2, 16, 128), (2, 1, 128, 5000)])
