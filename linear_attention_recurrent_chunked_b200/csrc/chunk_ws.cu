@@ -738,7 +738,10 @@ __global__ void __launch_bounds__(NT_WS, 1)
     //    transition grid, so output CTAs run beside transition CTAs that still run or fold;
     //  * otherwise the preceding grid (the loader, after starting the first chunks' Q, K, V loads).
     griddep_launch();
-    if (*err & ERRBIT_SEQLENS) return;
+    if (*err & ERRBIT_SEQLENS) {
+        griddep_wait();  // the grids before this one end first here too: a kernel after the last may reuse the error word
+        return;
+    }
     Segment sg;
     const int h = blockIdx.x;
     if (!find_segment(seg_off, cu, N, T_tot, blockIdx.y, seg_chunks * C, sg)) return;
@@ -1170,7 +1173,10 @@ __global__ void __launch_bounds__(NT_TRANS, 1)
     // in which the hardware dispatches the grid's blocks.
     if (threadIdx.x == 0) s_ticket = (int)atomicAdd(rec_flag + 1, 1u);
     __syncthreads();
-    if (*err & ERRBIT_SEQLENS) return;
+    if (*err & ERRBIT_SEQLENS) {
+        griddep_wait();  // the grids before this one end first here too: a kernel after the last may reuse the error word
+        return;
+    }
     Segment sg;
     const int h = s_ticket % H, gseg = s_ticket / H;
     if (!find_segment(seg_off, cu, N, T_tot, gseg, seg_chunks * C, sg) || sg.s == sg.ns - 1) {

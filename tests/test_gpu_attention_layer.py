@@ -610,3 +610,33 @@ def test_layer_chain_without_gaps_and_in_a_graph():
         g.replay()
         torch.cuda.synchronize()
         assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("T,H", [(2048, 4), (700, 2)])
+def test_layer_after_a_recurrent_layer(T, H):
+    """A recurrent layer's pack, whose last kernel lets the next one start early, then an attention layer on its output
+    with the same workspace: the same bits as with the device idle in between; and after a malformed pack, which
+    that layer reports and does not write, the attention layer's own error word."""
+    gen = torch.Generator().manual_seed(32)
+    q, k = (torch.nn.functional.normalize(torch.randn(T, H, 128, generator=gen), dim=-1).to(BF).cuda() for _ in range(2))
+    v = randn(gen, T, H, 128).cuda()
+    g, beta = (-torch.rand(T, H, generator=gen)).cuda(), torch.rand(T, H, generator=gen).cuda()
+    good = torch.tensor([0, T // 3, T], dtype=torch.int32).cuda()
+    bad = torch.tensor([0, T, T // 3], dtype=torch.int32).cuda()
+    pos = torch.arange(T, dtype=torch.int32).cuda()
+    ws = torch.zeros(gdn.chunk_fwd_workspace_size(2, T, H, 128, 128, BF), dtype=torch.uint8, device="cuda")
+
+    def run(sync, cu, check):
+        o = torch.full_like(v, 3.0)
+        gdn.chunk_fwd(q, k, v, g, beta, cu_seqlens=cu, o=o, workspace=ws)
+        sync()
+        x, y = gdn.qk_norm_rope(o, k, None, None, pos, workspace=ws)
+        sync()
+        return o, gdn.attn_prefill(x, y, o, good, max_len=T, workspace=ws, check=check)
+
+    for cu in (good, bad):
+        want = run(torch.cuda.synchronize, cu, True)
+        assert torch.isfinite(want[1]).all() and bool((want[0] == 3.0).all()) == (cu is bad)
+        for _ in range(20):
+            got = run(lambda: None, cu, True)
+            assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
