@@ -324,7 +324,8 @@ gdn_status gdn_qk_norm_rope(const void *q, int64_t q_stride, const void *k, int6
  *   scale > 0, or <= 0 for 1 / sqrt(d)
  *   workspace, ws_bytes: >= 256 bytes (also GDN_ERR_TIMEOUT if a bounded wait gave up).
  * The scores stay in tensor memory. A sequence's outputs depend on its own rows alone, whatever values
- * (NaN included) its neighbours in the pack hold. One kernel.
+ * (NaN included) its neighbours in the pack hold. Within a sequence a key (NaN included) does not reach
+ * earlier tokens either; a value that is not finite may, as weight 0 times it. One kernel.
  */
 gdn_status gdn_attn_prefill(const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v,
                             int64_t v_stride, const int32_t *cu_seqlens, int N, int T_tot, int Hq, int Hkv, int d,

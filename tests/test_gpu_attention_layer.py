@@ -297,6 +297,20 @@ def test_prefill_neighbours_do_not_leak(d):
         assert torch.equal(got[a:b], want[a:b])
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("at", [1, 63, 64, 130, 299])
+def test_prefill_later_queries_and_keys_do_not_reach_back(at, d):
+    """NaN and infinity in later tokens' queries and keys leave the earlier ones as they were, bit for bit."""
+    gen = torch.Generator().manual_seed(17)
+    q, k, v, _ = (x.cuda() for x in prompt(gen, [300], 4, 2, d))
+    v = v[:, 6:]
+    want = gdn.attn_prefill(q, k, v, check=True)
+    for value in (float("nan"), float("inf"), -float("inf")):
+        q2, k2 = q.clone(), k.clone()
+        q2[at:], k2[at:] = value, value
+        assert torch.equal(gdn.attn_prefill(q2, k2, v, check=True)[:at], want[:at])
+
+
 def test_prefill_malformed_seqlens_reported_not_written():
     gen = torch.Generator().manual_seed(8)
     q, k, v, _ = prompt(gen, [256], 4, 2, 128)
