@@ -22,10 +22,11 @@
 // is: with few tokens (a decode step) each warp has one group of rows; with many a warp walks through
 // tokens, computes a token's sines and cosines once for all of its heads there (a lane keeps the same
 // columns for every row), loads the next rows while it works on these and asks L2 for those a token on.
-// 10240 tokens, 16 + 4 heads of 128 in bf16, keys and values cached: 136 MB in 28.1 us (4.85 TB/s; a plain
+// 10240 tokens, 16 + 4 heads of 128 in bf16, keys and values cached: 136 MB in 27.5 us (4.96 TB/s; a plain
 // copy of as many bytes takes 23.4 us), issue slots 58 % busy. One run a lane with shuffled partners, a token a
 // warp: 40 us; at 29.5 us, without the L2 prefetch 33; with 3 CTAs per SM 30.1, with 5 (two row groups no longer
-// fit the registers) 32.7. A decode step's 64 tokens: 2.7 us, a launch.
+// fit the registers) 32.7; at 28.0, with the prefetch two tokens ahead 30.3, and 27.5 once the loads were hinted as
+// first out of L2. A decode step's 64 tokens: 2.7 us, a launch.
 #include <math.h>
 
 #include <algorithm>
@@ -141,8 +142,9 @@ __global__ void __launch_bounds__(kWarps * 32, kResident) k_norm_rope(const __gr
         for (int i = 0; i < kUnroll; ++i) {
             next[i][0] = next[i][1] = make_uint4(0, 0, 0, 0);
             if (i < next_n && i * RPW < heads) {
-                next[i][0] = *reinterpret_cast<const uint4 *>(src + i * STEP);
-                next[i][1] = *reinterpret_cast<const uint4 *>(src + i * STEP + to_b);
+                // (first out of L2: nothing here reads them again)
+                next[i][0] = __ldcs(reinterpret_cast<const uint4 *>(src + i * STEP));
+                next[i][1] = __ldcs(reinterpret_cast<const uint4 *>(src + i * STEP + to_b));
                 if (left > groups) {  // the next token's, on their way to L2
                     asm volatile("prefetch.global.L2 [%0];" ::"l"(src + i * STEP + stride));
                     asm volatile("prefetch.global.L2 [%0];" ::"l"(src + i * STEP + to_b + stride));
