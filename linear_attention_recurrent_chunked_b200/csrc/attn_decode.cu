@@ -17,8 +17,9 @@
 // (by 16-byte asynchronous copies a step took 750 cycles to ask for, as long as all of its arithmetic). The
 // products are S^T = K Q^T and O^T = V^T P^T on m16n8k16 tensor instructions: the 16 keys (or 16 of the d
 // columns) are the rows and the heads the 8 columns, so a group of up to 8 heads wastes nothing on padding
-// rows, which a 128-row tile would; at these few flops a byte the memory stays the bound. A run cuts at most its first and last (sequence, head) short: those pieces are joined over the
-// CTA's warps once at the end, and what even the CTA's run cuts short goes to the CTA's two slots.
+// rows, which a 128-row tile would; at these few flops a byte the memory stays the bound. A run cuts at most
+// its first and last (sequence, head) short: those pieces are joined over the CTA's warps once at the end, and
+// what even the CTA's run cuts short goes to the CTA's two slots.
 //
 // The prefix runs in the prompt kernel (attn_prefill.cu) without a mask, all sequences' query heads of a
 // key head as rows of one tile, so its keys are read once per 128 rows and not once per sequence.
@@ -723,6 +724,7 @@ cudaError_t launch_attn_decode(const AttnDecode &a, int d, cudaStream_t st, cons
         const cudaError_t e = launch_attn_prefix(p, d, st, stage);
         if (e != cudaSuccess) return e;
     }
+    // groups of more than 8 heads take two tiles of 8 columns
     if (d == 64) return a.G <= 8 ? launch<64, 1>(a, st, stage) : launch<64, 2>(a, st, stage);
     return a.G <= 8 ? launch<128, 1>(a, st, stage) : launch<128, 2>(a, st, stage);
 }
