@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+from threading import get_ident
 from typing import Optional
 
 import torch
@@ -273,16 +274,18 @@ def _index(name, t):
 
 
 def _stream_and_ws(index, nbytes, workspace):
-    """The current stream of a device, and a workspace: the caller's, or the cached one of this device
-    and stream, or while a graph is being captured a fresh one, so that the graph keeps memory of its own."""
+    """The current stream of a device, and a workspace: the caller's, or the cached one of this device, stream
+    and thread (the kernels of two threads' calls on one stream may take turns), or while a graph is being captured a
+    fresh one, so that the graph keeps memory of its own."""
     stream = torch._C._cuda_getCurrentRawStream(index)
     if workspace is None:
         if torch._C._cuda_isCurrentStreamCapturing():
             workspace = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=torch.device("cuda", index))
         else:
-            workspace = _ws_cache.get((index, stream))
+            key = (index, stream, get_ident())
+            workspace = _ws_cache.get(key)
             if workspace is None or workspace.numel() < nbytes:
-                workspace = _workspace(nbytes, torch.device("cuda", index))
+                workspace = _ws_cache[key] = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=torch.device("cuda", index))
         return stream, workspace, workspace.numel()
     if not workspace.is_contiguous() or workspace.get_device() != index:
         raise GdnError(6, "workspace must be a contiguous tensor on the inputs' device")

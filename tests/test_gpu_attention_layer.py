@@ -9,6 +9,8 @@ Bounds, per element (u = 2^-8 the half step of bf16, e = 2^-24 that of fp32):
   scores' fp32 sums, 2 d e |scale| max|q| max|k| each (the tensor core may truncate: 2 e a step),
   which moves a weight against the others by twice that; the sums over the n keys, 2 n e a.
 """
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -654,3 +656,26 @@ def test_layer_after_a_recurrent_layer(T, H):
         for _ in range(20):
             got = run(lambda: None, cu, True)
             assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_two_threads_on_one_stream():
+    """Two threads call the operators on the same stream at once, with kernels of one call between those of another:
+    each gets the bits of calls made alone."""
+    gen = torch.Generator().manual_seed(33)
+    works = [on_gpu(cached(gen, [200, 33, 0, 600, 5], 8, 2, 128, 16, 300)), on_gpu(cached(gen, [90] * 60, 16, 4, 64, 32, 1000))]
+    want = [gdn.attn_decode(**w) for w in works]
+    torch.cuda.synchronize()
+    start, wrong = threading.Barrier(2), []
+
+    def serve(w, y):
+        start.wait()
+        got = [gdn.attn_decode(**w) for _ in range(200)]
+        torch.cuda.current_stream().synchronize()
+        wrong.append(sum(not torch.equal(x, y) for x in got))
+
+    threads = [threading.Thread(target=serve, args=(w, y)) for w, y in zip(works, want)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert wrong == [0, 0]
