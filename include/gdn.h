@@ -282,7 +282,8 @@ gdn_status gdn_attn_fwd(const void *q, const void *k, const void *v, const int32
  *     128; slot s is place s % page_size of page s / page_size. num_pages page_size <= 2^31 - 1.
  *   - workspace: the error word (and what the entry point says), as elsewhere; gdn_chunk_fwd_check
  *     reads it. Calls that overlap on the GPU, replays of captured graphs among them, must not share
- *     a workspace. Index arrays (int32) are 4-byte aligned.
+ *     a workspace, nor may calls that two threads make on one stream, whose kernels may take turns. Index
+ *     arrays (int32) are 4-byte aligned.
  *   - Outputs that overlap inputs in another way than an entry point allows are refused
  *     (GDN_ERR_SHAPE), caches excepted: k_cache and v_cache must not overlap anything else.
  *   - The first call on a device may load the library's module: make it before any stream capture.
