@@ -351,8 +351,9 @@ gdn_status gdn_attn_prefill(const void *q, int64_t q_stride, const void *k, int6
  *   workspace    gdn_attn_decode_workspace_size(...) bytes, 256-byte aligned; contents on entry ignored
  * A length or page number outside its range is recorded as GDN_ERR_PAGES: lengths are taken to the
  * nearest bound and such a page reads as zeros, so that no access leaves the cache, and the outputs
- * concerned are meaningless. What stale slots hold (NaN included) does not matter. Equal calls give
- * equal bits.
+ * concerned are meaningless. What stale slots hold (NaN included) does not matter. A key whose score is
+ * minus infinity has weight zero; a sequence that has keys but no other score than that is NaN. Equal calls
+ * give equal bits.
  */
 size_t gdn_attn_decode_workspace_size(int B, int Hq, int Hkv, int d, int prefix_len);
 gdn_status gdn_attn_decode(const void *q, const void *k_cache, const void *v_cache, int num_pages, int page_size,

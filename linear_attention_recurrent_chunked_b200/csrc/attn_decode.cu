@@ -343,7 +343,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                         m[t][i] = mt[i];
                         grow = true;
                     }
-                    const float p0 = chunk::ex2(s[t][i] - m[t][i]), p1 = chunk::ex2(s[t][i + 2] - m[t][i]);
+                    // (no finite score yet, m = -inf: those weights are zero too, and -inf - -inf would be NaN)
+                    const float ref = m[t][i] == -INFINITY ? 0.f : m[t][i];
+                    const float p0 = chunk::ex2(s[t][i] - ref), p1 = chunk::ex2(s[t][i + 2] - ref);
                     l[t][i] = l[t][i] * alpha[i] + p0 + p1;
                     s[t][i] = p0;
                     s[t][i + 2] = p1;
