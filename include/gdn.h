@@ -326,7 +326,8 @@ gdn_status gdn_qk_norm_rope(const void *q, int64_t q_stride, const void *k, int6
  *   workspace, ws_bytes: >= 256 bytes (also GDN_ERR_TIMEOUT if a bounded wait gave up).
  * The scores stay in tensor memory. A sequence's outputs depend on its own rows alone, whatever values
  * (NaN included) its neighbours in the pack hold. Within a sequence a key (NaN included) does not reach
- * earlier tokens either; a value that is not finite may, as weight 0 times it. One kernel.
+ * earlier tokens either; a value that is not finite may, as weight 0 times it. A key whose score is minus
+ * infinity has weight zero; a row whose scores are all of that kind is NaN. One kernel.
  */
 gdn_status gdn_attn_prefill(const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v,
                             int64_t v_stride, const int32_t *cu_seqlens, int N, int T_tot, int Hq, int Hkv, int d,

@@ -371,8 +371,7 @@ __global__ void __launch_bounds__(NTHREADS, 2)
 #pragma unroll
             for (int i = 8; i < STEP; i += 2) pm[(i >> 1) & 3] = attn::max3(pm[(i >> 1) & 3], S(i), S(i + 1));
             const float mt = attn::max3(fmaxf(pm[0], pm[1]), pm[2], pm[3]) * sc;
-            // lazy rescale: a new reference maximum only when this step's exceeds it by more than kRescale. (A step
-            // may be masked whole for a row, mt = -inf, but never the first one.)
+            // lazy rescale: a new reference maximum only when this step's exceeds it by more than kRescale
             float alpha = 1.f;
             const bool grow = mt > m_ref + kRescale;
             if (grow) {
@@ -395,7 +394,9 @@ __global__ void __launch_bounds__(NTHREADS, 2)
             }
             // the weights as bf16 pairs
             uint64_t ps[2] = {0, 0};
-            const uint64_t sc2 = attn::pack2(sc, sc), mm2 = attn::pack2(-m_ref, -m_ref);
+            // (no finite score yet, m_ref = -inf: those weights are zero too, and -inf - -inf would be NaN)
+            const float m0 = m_ref == -INFINITY ? 0.f : -m_ref;
+            const uint64_t sc2 = attn::pack2(sc, sc), mm2 = attn::pack2(m0, m0);
             uint32_t w[32];
 #pragma unroll
             for (int i = 0; i < 32; ++i) {

@@ -3,8 +3,9 @@ tests/test_gpu_attention_layer.py derives."""
 import pytest
 import torch
 
+from oracle import attention_layer as al
 from linear_attention_recurrent_chunked_b200 import gdn
-from tests.test_gpu_attention_layer import cached, check_decode, on_gpu
+from tests.test_gpu_attention_layer import attn_tol, cached, check_decode, close, on_gpu, prompt
 
 pytestmark = pytest.mark.gpu
 INF = float("inf")
@@ -51,3 +52,41 @@ def test_decode_sequence_with_no_finite_score(prefix):
     o = gdn.attn_decode(**on_gpu(w), check=True)
     assert torch.isnan(o[1]).all()
     check_decode(dict(w, q=w["q"][::2], page_table=w["page_table"][::2], lens=w["lens"][::2]), got=o[::2])
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("Hq,Hkv", [(4, 2), (3, 1)])
+@pytest.mark.parametrize("low", [64, 70, 200])
+def test_prefill_first_keys_at_minus_infinity_weigh_nothing(low, Hq, Hkv, d):
+    """A prompt whose first keys all have the score minus infinity: later rows see the other keys alone, the rows
+    that see none but those are 0 / 0."""
+    T = 330
+    gen = torch.Generator().manual_seed(low + d)
+    q, k, v, _ = prompt(gen, [T], Hq, Hkv, d)
+    v = v[:, Hq + Hkv:].contiguous()
+    q[..., 0] = -q[..., 0].abs() - 0.5
+    k[:low, :, 0] = INF
+    o = gdn.attn_prefill(q.cuda(), k.cuda(), v.cuda(), check=True)
+    assert torch.isnan(o[:low]).all()
+    ref, a = al.prompt_attention(q, k, v, [T])
+    close(o[low:], ref[low:], attn_tol(ref, a, q, torch.nan_to_num(k, 0.0, 0.0, 0.0), d, T)[low:])
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("low", [64, 200, 500])
+def test_decode_prefix_keys_at_minus_infinity_weigh_nothing(low, d):
+    """The shared prefix starts with keys at minus infinity, down to all of it: then the own keys alone count, and a
+    sequence without any is 0 / 0."""
+    prefix, page = 500, 16
+    gen = torch.Generator().manual_seed(low + d)
+    w = cached(gen, [5, 40, 0, 200], 8, 2, d, page, prefix)
+    w["q"][..., 0] = -w["q"][..., 0].abs() - 0.5
+    for t in range(low):
+        w["k_cache"][int(w["prefix_pages"][t // page]), :, t % page, 0] = INF
+    if low < prefix:
+        check_decode(w)
+        return
+    o = gdn.attn_decode(**on_gpu(w), check=True)
+    assert torch.isnan(o[2]).all()
+    rows = [0, 1, 3]
+    check_decode(dict(w, q=w["q"][rows], page_table=w["page_table"][rows], lens=w["lens"][rows]), got=o[rows])
