@@ -419,7 +419,10 @@ __global__ void __launch_bounds__(NTHREADS, 2)
             if (it.keys - j * STEP < STEP) {
                 // rows of V beyond the sequence or the prefix: another sequence's values or stale slots
                 const int c = 2 * j + 1, st = c % L::NST, n = it.keys - j * STEP;
-                if (!(ok = wait_bar_w(&bar[L::FULL + st], (uint32_t)((c / L::NST) & 1), ctl, a.err))) break;
+                if (!(ok = wait_bar_w(&bar[L::FULL + st], (uint32_t)((c / L::NST) & 1), ctl, a.err))) {
+                    tc::tmem_st_wait();  // the weights' store must end before the tensor memory goes
+                    break;
+                }
                 if (r >= n && r < STEP) {
 #pragma unroll
                     for (int hf = 0; hf < D / 64; ++hf)
