@@ -420,9 +420,21 @@ gdn_status gdn_diag_ut_solve(const float *A, float *T, void *stream);
  *     too, record GDN_ERR_TIMEOUT in the workspace's error word and return.
  *     Outputs of the affected (sequence, head) pairs are then incomplete;
  *     other heads are unaffected. gdn_chunk_fwd_check reports the timeout.
+ *   GDN_INJECT_WITHHOLD_KEYS, GDN_INJECT_WITHHOLD_VALUES: in every later
+ *     gdn_attn_prefill and gdn_attn_decode call, the first block of each kernel
+ *     does not load the keys, or values, of its second step of keys (each of its
+ *     warps of its own run in gdn_attn_decode's kernel of the own keys, keys and
+ *     values together; a block with one step is not affected). Its waits give up
+ *     after wait_us microseconds, the block ends without those results and
+ *     GDN_ERR_TIMEOUT is recorded; outputs that it has no part in are unaffected.
  * Returns GDN_ERR_SHAPE for an unknown kind or an out-of-range wait_us.
  */
-typedef enum { GDN_INJECT_NONE = 0, GDN_INJECT_WITHHOLD_LINK = 1 } gdn_inject_kind;
+typedef enum {
+    GDN_INJECT_NONE = 0,
+    GDN_INJECT_WITHHOLD_LINK = 1,
+    GDN_INJECT_WITHHOLD_KEYS = 2,
+    GDN_INJECT_WITHHOLD_VALUES = 3
+} gdn_inject_kind;
 gdn_status gdn_debug_inject(int kind, unsigned wait_us);
 
 /*

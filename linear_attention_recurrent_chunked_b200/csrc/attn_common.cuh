@@ -13,15 +13,16 @@
 namespace gdn {
 namespace attn {
 
-constexpr uint64_t kWaitNs = 1000000000ull;
+constexpr uint64_t kWaitNs = 1000000000ull;  // of a wait, but for tests of the give-up path (gdn_debug_inject)
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct Ctl {
     uint32_t tmem, abort;
+    uint64_t wait_ns;  // how long a wait may last
 };
 
 // Bounded wait for the phase `parity` of an mbarrier; gives up when another role has aborted, or
-// after kWaitNs (the error word is set and the CTA's other roles leave their loops too). The first
+// after ctl->wait_ns (the error word is set and the CTA's other roles leave their loops too). The first
 // test is inlined, the polling loop is a call.
 __device__ __noinline__ inline bool wait_bar_poll(uint64_t *bar, uint32_t parity, Ctl *ctl, uint32_t *err) {
     const uint64_t t0 = tc::globaltimer();
@@ -29,7 +30,7 @@ __device__ __noinline__ inline bool wait_bar_poll(uint64_t *bar, uint32_t parity
         if (tc::mbar_try_wait(bar, parity)) return true;
         if ((i & 15u) == 0) {
             if (*reinterpret_cast<volatile uint32_t *>(&ctl->abort)) return false;
-            if (tc::globaltimer() - t0 > kWaitNs) {
+            if (tc::globaltimer() - t0 > ctl->wait_ns) {
                 if (err) atomicOr(err, ERRBIT_TIMEOUT);
                 *reinterpret_cast<volatile uint32_t *>(&ctl->abort) = 1u;
                 return false;
@@ -45,10 +46,10 @@ __device__ __forceinline__ bool wait_bar_w(uint64_t *bar, uint32_t parity, Ctl *
     return __all_sync(0xffffffffu, wait_bar(bar, parity, ctl, err));
 }
 // Before a CTA that gave up may end: its own copies and products in flight (bounded too).
-__device__ __noinline__ inline void drain_bar(uint64_t *bar, uint32_t parity) {
+__device__ __noinline__ inline void drain_bar(uint64_t *bar, uint32_t parity, const Ctl *ctl) {
     const uint64_t t0 = tc::globaltimer();
     while (!tc::mbar_try_wait(bar, parity))
-        if (tc::globaltimer() - t0 > kWaitNs) return;
+        if (tc::globaltimer() - t0 > ctl->wait_ns) return;
 }
 
 // Every kernel here is launched to start while the one before it in the stream drains (launch_early): it sets

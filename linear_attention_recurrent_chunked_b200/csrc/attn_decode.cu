@@ -173,7 +173,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < S::NST; ++i) tc::mbar_init(&bars[warp][i], 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (tid == 0) ctl.abort = 0;
+    if (tid == 0) {
+        ctl.abort = 0;
+        ctl.wait_ns = a.wait_ns;
+    }
     // with a prefix its kernel comes before, whose CTAs have all waited already and whose results nothing here reads
     if (!a.prefix_len) grid_wait();
     grid_launch_dependents();
@@ -251,9 +254,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const bool there = page >= 0 && page < a.num_pages;
                 bad |= !there;
                 uint64_t *bar = &bars[warp][ld_st];
-                if (lane == 0) tc::mbar_arrive_expect_tx(bar, 2 * S::HALF);
+                const bool withheld = a.withhold && blockIdx.x == 0 && ld_u == u0 + 1;  // (tests of the give-up path)
+                if (lane == 0 && !withheld) tc::mbar_arrive_expect_tx(bar, 2 * S::HALF);
                 __syncwarp();
-                if (lane < 2 * (D / 64)) {  // K's and V's 64-column halves; a page that is none reads as zeros
+                if (lane < 2 * (D / 64) && !withheld) {  // K's and V's 64-column halves; a page that is none reads as zeros
                     const int kv = lane / (D / 64), hf = lane % (D / 64);
                     tc::tma_load_3d(ring + ld_st * 2 * S::HALF + kv * S::HALF + hf * (kStep * 128), kv ? &tm_v : &tm_k, bar, hf * 64,
                                     ld.chunk * kStep & ((1 << a.page_log) - 1), (there ? page : a.num_pages) * a.Hkv + ld.h);
@@ -285,13 +289,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             if (!attn::wait_bar_w(&bars[warp][st], phase, &ctl, nullptr)) {
-                // gave up (or another warp did): its own copies still have to land before the CTA may end
+                // gave up (or another warp did, and then this step's copy too may be under way): its own copies still
+                // have to land before the CTA may end
                 timed_out = true;
-                for (int i = 1; i < S::NST; ++i) {
+                for (int i = 0; i < S::NST; ++i) {
+                    if (lane == 0 && u + i < ld_u) attn::drain_bar(&bars[warp][st], phase, &ctl);
                     st = st + 1 == S::NST ? 0 : st + 1;
                     phase ^= st == 0;
-                    if (lane == 0 && u + i < ld_u) attn::drain_bar(&bars[warp][st], phase);
                 }
+                __syncwarp();
                 break;
             }
             const int n = at.len - at.chunk * kStep;  // keys of the step, at least 1; 16 or more: all
@@ -703,7 +709,10 @@ size_t attn_decode_slots(int B, int Hq, int Hkv, int prefix_len) {
     return (size_t)(Hq / Hkv) * 2 * kDecodeCtas + (prefix_len > 0 ? (size_t)B * Hq : 0);
 }
 
-cudaError_t launch_attn_decode(const AttnDecode &a, int d, cudaStream_t st, const char **stage) {
+cudaError_t launch_attn_decode(AttnDecode a, int d, cudaStream_t st, const char **stage) {
+    const Inject inj = inject_settings();
+    a.wait_ns = inj.wait_ns ? inj.wait_ns : attn::kWaitNs;
+    a.withhold = inj.withhold_tile;
     if (a.prefix_len > 0) {
         AttnPrefill p{};
         p.q = a.q;
@@ -723,6 +732,8 @@ cudaError_t launch_attn_decode(const AttnDecode &a, int d, cudaStream_t st, cons
         p.splits = a.splits;
         p.part_o = a.part_o;
         p.part_ml = a.part_ml;
+        p.wait_ns = a.wait_ns;
+        p.withhold = a.withhold;
         const cudaError_t e = launch_attn_prefix(p, d, st, stage);
         if (e != cudaSuccess) return e;
     }

@@ -254,6 +254,7 @@ __global__ void __launch_bounds__(NTHREADS, 2)
     if (tid == W_LOAD * 32) {
         for (int i = 0; i < L::NBAR; ++i) tc::mbar_init(&bar[i], (i >= L::SFREE && i < L::PVD) ? 4u : i == L::FIN ? 2u : 1u);
         ctl->abort = 0;
+        ctl->wait_ns = a.wait_ns;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     tc::fence_before_sync();
@@ -289,11 +290,12 @@ __global__ void __launch_bounds__(NTHREADS, 2)
             for (int kv = 0; kv < 2; ++kv, ++c) {
                 const int st = c % L::NST;
                 if (c >= L::NST && !(ok = wait_bar_w(&bar[L::EMPTY + st], (uint32_t)((c / L::NST - 1) & 1), ctl, a.err))) break;
-                if (lane == 0) tc::mbar_arrive_expect_tx(&bar[L::FULL + st], L::KTILE);
+                const bool withheld = a.withhold && c == a.withhold && blockIdx.x == 0;  // (tests of the give-up path)
+                if (lane == 0 && !withheld) tc::mbar_arrive_expect_tx(&bar[L::FULL + st], L::KTILE);
                 __syncwarp();
                 const CUtensorMap *map = kv ? &tm_v : &tm_k;
                 const uint32_t dst = sb + L::OFF_KV + st * L::KTILE + lane * rows * 128;
-                if (lane < boxes) {
+                if (lane < boxes && !withheld) {
 #pragma unroll
                     for (int hf = 0; hf < D / 64; ++hf) {
                         if (MODE == PREFIX)
@@ -307,8 +309,8 @@ __global__ void __launch_bounds__(NTHREADS, 2)
             if (MODE == PREFIX && j + 1 < it.ns) page = page_of(j + 1);
         }
         if (lane == 0) {
-            attn::drain_bar(&bar[L::QFULL], 0);
-            for (int i = std::max(c - L::NST, 0); i < c; ++i) attn::drain_bar(&bar[L::FULL + i % L::NST], (i / L::NST) & 1);
+            attn::drain_bar(&bar[L::QFULL], 0, ctl);
+            for (int i = std::max(c - L::NST, 0); i < c; ++i) attn::drain_bar(&bar[L::FULL + i % L::NST], (i / L::NST) & 1, ctl);
         }
         __syncwarp();
     } else if (warp >= W_S) {
@@ -318,7 +320,7 @@ __global__ void __launch_bounds__(NTHREADS, 2)
             o_loop<D>(it.ns, tm, sb, bar, ctl, a.err);
         // tensor memory may go once every product is done
         tc::mma_commit_w(&bar[L::FIN]);
-        if (lane == 0) attn::drain_bar(&bar[L::FIN], 0);
+        if (lane == 0) attn::drain_bar(&bar[L::FIN], 0, ctl);
         __syncwarp();
     } else {
         // ---------------------------------------------------------------- softmax (one query row per thread)
@@ -536,7 +538,10 @@ cudaError_t launch_attn_prefix(const AttnPrefill &a, int d, cudaStream_t st, con
     return d == 64 ? launch_prefix<64>(a, st, stage) : launch_prefix<128>(a, st, stage);
 }
 
-cudaError_t launch_attn_prefill(const AttnPrefill &a, int d, cudaStream_t st, const char **stage) {
+cudaError_t launch_attn_prefill(AttnPrefill a, int d, cudaStream_t st, const char **stage) {
+    const Inject inj = inject_settings();
+    a.wait_ns = inj.wait_ns ? inj.wait_ns : attn::kWaitNs;
+    a.withhold = inj.withhold_tile;
     if (a.T_tot == 0 || a.max_len == 0) {
         // nothing to compute: only the error word (cu_seqlens must then be all zeros)
         *stage = "error word";

@@ -157,7 +157,11 @@ std::atomic<unsigned long long> g_inject_wait_ns{0};
 
 Inject inject_settings() {
     const int kind = g_inject_kind.load(std::memory_order_relaxed);
-    return Inject{kind == GDN_INJECT_WITHHOLD_LINK, kind ? (uint64_t)g_inject_wait_ns.load() : 0ull};
+    const uint64_t ns = g_inject_wait_ns.load();
+    if (kind == GDN_INJECT_WITHHOLD_LINK) return Inject{true, ns, 0, 0};
+    if (kind == GDN_INJECT_WITHHOLD_KEYS) return Inject{false, 0, 2, ns};
+    if (kind == GDN_INJECT_WITHHOLD_VALUES) return Inject{false, 0, 3, ns};
+    return Inject{};
 }
 
 // Sets the calling thread's last-error message (for entry points defined in other files).
@@ -623,7 +627,7 @@ gdn_status gdn_attn_decode(const void *q, const void *k_cache, const void *v_cac
 }
 
 gdn_status gdn_debug_inject(int kind, unsigned wait_us) {
-    if (kind != GDN_INJECT_NONE && kind != GDN_INJECT_WITHHOLD_LINK)
+    if (kind < GDN_INJECT_NONE || kind > GDN_INJECT_WITHHOLD_VALUES)
         return fail(GDN_ERR_SHAPE, "unknown injection kind %d", kind);
     if (kind != GDN_INJECT_NONE && (wait_us == 0 || wait_us > 1000000u))
         return fail(GDN_ERR_SHAPE, "wait_us=%u outside 1 .. 1000000", wait_us);

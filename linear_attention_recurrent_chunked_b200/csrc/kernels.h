@@ -96,11 +96,13 @@ struct AttnPrefill {
     int num_pages, page_log, prefix_len, splits;
     float *part_o;    // [splits][B][Hq][d] unnormalised
     float2 *part_ml;  // [splits][B][Hq] reference maximum (log2 units) and sum
-    int P, blocks;    // set by the launcher: positions per query tile, query tiles of the longest sequence
-    bool dense;       // also: blocks numbered sequence by sequence
+    uint64_t wait_ns;  // set by the launcher, as all below: how long a wait may last
+    int withhold;      // (tests) the tile of the ring that the first CTA does not load, or 0
+    int P, blocks;    // positions per query tile, query tiles of the longest sequence
+    bool dense;       // blocks numbered sequence by sequence
 };
 int64_t attn_prefill_tiles(int T_tot, int N, int P);  // most query tiles that N sequences of T_tot tokens can have
-cudaError_t launch_attn_prefill(const AttnPrefill &a, int d, cudaStream_t st, const char **stage);
+cudaError_t launch_attn_prefill(AttnPrefill a, int d, cudaStream_t st, const char **stage);
 
 // The same kernel without the mask over a cached prefix that a batch shares: partial results per split.
 cudaError_t launch_attn_prefix(const AttnPrefill &a, int d, cudaStream_t st, const char **stage);
@@ -121,18 +123,24 @@ struct AttnDecode {
     float *part_o;  // the prefix kernel's, per split
     float2 *part_ml;
     uint32_t *bad;  // [kDecodeCtas] the error bits of each CTA
-    int rows;       // set by the launcher: query heads that a CTA of the combine kernel takes
+    int rows;       // set by the launcher, as all below: query heads that a CTA of the combine kernel takes
+    int withhold;   // (tests) not 0: the first CTA's warps do not load the second step of their runs
+    uint64_t wait_ns;  // how long a wait may last
 };
 int attn_decode_splits(int B, int Hq, int Hkv, int prefix_len);
 size_t attn_decode_slots(int B, int Hq, int Hkv, int prefix_len);  // rows of d floats
-cudaError_t launch_attn_decode(const AttnDecode &a, int d, cudaStream_t st, const char **stage);
+cudaError_t launch_attn_decode(AttnDecode a, int d, cudaStream_t st, const char **stage);
 
 // Failure injection for tests (set by gdn_debug_inject; off by default): the pipelined path's
 // first segment of head 0 withholds its end-state flag, and waits for flags give up after
-// flag_wait_ns (0 = the normal bound) instead of hanging.
+// flag_wait_ns (0 = the normal bound) instead of hanging; or the grouped-head attention kernels' first
+// CTA withholds a load (tile 2, the keys of its second step, or 3, their values; 0 = none) and all of their
+// waits give up after wait_ns (0 = the normal bound).
 struct Inject {
     bool withhold_first_link;
     uint64_t flag_wait_ns;
+    int withhold_tile;
+    uint64_t wait_ns;
 };
 Inject inject_settings();
 

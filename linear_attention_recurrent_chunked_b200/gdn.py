@@ -524,7 +524,8 @@ def diag_mma_tile(A, B, a_mn: int = 0, b_mn: int = 0, variant: int = 0):
 
 def debug_inject(kind: int, wait_us: int = 0) -> None:
     """Failure injection for tests (see include/gdn.h): 0 = off, 1 = withhold the first
-    segment's end state of head 0 so that the blocks waiting for it time out after wait_us."""
+    segment's end state of head 0 so that the blocks waiting for it time out after wait_us; 2, 3 =
+    withhold a load of keys or values in the attention layer's kernels likewise."""
     _check(load_library().gdn_debug_inject(kind, wait_us))
 
 

@@ -1,5 +1,7 @@
 """Edges of the attention layer's operators, against the fp64 oracle with the bounds that
 tests/test_gpu_attention_layer.py derives."""
+import time
+
 import pytest
 import torch
 
@@ -90,3 +92,56 @@ def test_decode_prefix_keys_at_minus_infinity_weigh_nothing(low, d):
     assert torch.isnan(o[2]).all()
     rows = [0, 1, 3]
     check_decode(dict(w, q=w["q"][rows], page_table=w["page_table"][rows], lens=w["lens"][rows]), got=o[rows])
+
+
+# ------------------------------------------------------------------ waits that run out
+
+def given_up(kind, call):
+    """Runs a call of which one load is withheld: it must report the time-out, soon."""
+    gdn.debug_inject(kind, 20000)
+    try:
+        t0 = time.perf_counter()
+        with pytest.raises(gdn.GdnError) as e:
+            call()
+        assert e.value.status == 8 and time.perf_counter() - t0 < 5.0
+    finally:
+        gdn.debug_inject(0, 0)
+
+
+@pytest.mark.parametrize("kind", [2, 3])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("lens", [[100], [700], [640, 130, 20], [2500] + [9] * 80])
+def test_prefill_wait_that_runs_out(lens, d, kind):
+    """Keys, or values, of the first block that never come: its outputs are not written, the time-out is reported,
+    every other block's outputs are those of an undisturbed call, and so are the next call's. (The last pack numbers
+    its tiles sequence by sequence; the first one's withheld values are a sequence's last.)"""
+    gen = torch.Generator().manual_seed(50 + d)
+    Hq, Hkv, T = 8, 2, sum(lens)
+    q, k, v, cu = (x.cuda() for x in prompt(gen, lens, Hq, Hkv, d))
+    v = v[:, Hq + Hkv:]
+    want = gdn.attn_prefill(q, k, v, cu, max_len=max(lens), check=True)
+    o = torch.full_like(want, 3.0)
+    given_up(kind, lambda: gdn.attn_prefill(q, k, v, cu, max_len=max(lens), o=o, check=True))
+    first = (lens[0] - 1) // 32 * 32  # a tile has 32 positions of 4 heads; the longest one's block comes first
+    assert (o[first:lens[0], :4] == 3.0).all()
+    rest = torch.ones((T, Hq), dtype=torch.bool, device="cuda")
+    rest[first:lens[0], :4] = False
+    assert torch.equal(o[rest], want[rest])
+    assert torch.equal(gdn.attn_prefill(q, k, v, cu, max_len=max(lens), check=True), want)
+
+
+@pytest.mark.parametrize("kind", [2, 3])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("Hq,Hkv,prefix", [(16, 4, 0), (9, 1, 0), (16, 4, 6000), (16, 1, 3000)])
+def test_decode_wait_that_runs_out(Hq, Hkv, prefix, d, kind):
+    """The same for one token per sequence: the first block of the own keys' kernel, and of the prefix's."""
+    gen = torch.Generator().manual_seed(60 + d)
+    w = on_gpu(cached(gen, [2000] * (160 // Hkv), Hq, Hkv, d, 16, prefix))
+    want = gdn.attn_decode(**w, check=True)
+    o = torch.full_like(want, 3.0)
+    given_up(kind, lambda: gdn.attn_decode(**w, o=o, check=True))
+    # the first block's run of 1/148 of the keys lies within the first two sequences; the prefix's first block has rows
+    # of the first key head and of the sequences that fill 128 rows
+    n = 128 // (Hq // Hkv) if prefix else 2
+    assert torch.equal(o[n:], want[n:]) and torch.equal(o[2:, Hq // Hkv:], want[2:, Hq // Hkv:])
+    assert torch.equal(gdn.attn_decode(**w, check=True), want)
