@@ -31,6 +31,9 @@
  *   - Supported head sizes: dk = dv in {64, 128}.
  *   - o is written in the input dtype (bf16: rounded to nearest even from the
  *     fp32 accumulator). States are fp32.
+ *   - A workspace belongs to one call at a time: calls that overlap on the GPU, replays of captured graphs
+ *     among them, must not share one, nor may calls that two threads make on one stream, whose kernels
+ *     may take turns there. A graph keeps the workspace that its call was captured with.
  *   - NaN/Inf inputs are undefined behaviour; they are not checked on the hot
  *     path. Decays below ~1e-38 may be flushed to zero.
  *   - Errors are returned as gdn_status, never thrown or trapped;
@@ -82,7 +85,6 @@ const char *gdn_last_error(void);
  * without records. The workspace is
  * scratch owned by the caller: its contents on entry are ignored and on exit
  * are meaningless except for the error word read by gdn_chunk_fwd_check.
- * Two calls that overlap on the GPU must not share a workspace.
  */
 size_t gdn_chunk_fwd_workspace_size(int N, int T_tot, int H, int dk, int dv, gdn_dtype dtype);
 
@@ -281,9 +283,7 @@ gdn_status gdn_attn_fwd(const void *q, const void *k, const void *v, const int32
  *   - The cache of a layer is k_cache, v_cache [num_pages][Hkv][page_size][d], page_size 16, 32, 64 or
  *     128; slot s is place s % page_size of page s / page_size. num_pages page_size <= 2^31 - 1.
  *   - workspace: the error word (and what the entry point says), as elsewhere; gdn_chunk_fwd_check
- *     reads it. Calls that overlap on the GPU, replays of captured graphs among them, must not share
- *     a workspace, nor may calls that two threads make on one stream, whose kernels may take turns. Index
- *     arrays (int32) are 4-byte aligned.
+ *     reads it. Index arrays (int32) are 4-byte aligned.
  *   - Outputs that overlap inputs in another way than an entry point allows are refused
  *     (GDN_ERR_SHAPE), caches excepted: k_cache and v_cache must not overlap anything else.
  *   - The first call on a device may load the library's module: make it before any stream capture.

@@ -111,13 +111,43 @@ def chunk_fwd_workspace_size(N: int, T_tot: int, H: int, dk: int, dv: int, dtype
 _ws_cache = {}
 
 
-def _workspace(nbytes: int, device) -> torch.Tensor:
-    key = (device.index, torch.cuda.current_stream(device).cuda_stream)
-    ws = _ws_cache.get(key)
-    if ws is None or ws.numel() < nbytes:
-        ws = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
-        _ws_cache[key] = ws
-    return ws
+def _bytes(n, index):
+    return torch.empty(n, dtype=torch.uint8, device=torch.device("cuda", index))
+
+
+def _stream_and_ws(index, nbytes, workspace):
+    """The current stream of a device, and a workspace: the caller's, or the cached one of this device, stream
+    and thread (the kernels of two threads' calls on one stream may take turns), or while a graph is being captured a
+    fresh one, so that the graph keeps memory of its own."""
+    stream = torch._C._cuda_getCurrentRawStream(index)
+    if workspace is None:
+        if torch._C._cuda_isCurrentStreamCapturing():
+            workspace = _bytes(max(nbytes, 256), index)
+        else:
+            key = (index, stream, get_ident())
+            workspace = _ws_cache.get(key)
+            if workspace is None or workspace.numel() < nbytes:
+                workspace = _ws_cache[key] = _bytes(max(nbytes, 256), index)
+        return stream, workspace, workspace.numel()
+    if not workspace.is_contiguous() or workspace.get_device() != index:
+        raise GdnError(6, "workspace must be a contiguous tensor on the inputs' device")
+    return stream, workspace, workspace.numel() * workspace.element_size()
+
+
+class _Nothing:
+    def __enter__(self):
+        return None
+
+    def __exit__(self, *exc):
+        return False
+
+
+_NOTHING = _Nothing()
+
+
+def _on(index):
+    """Makes the tensors' device the current one for a call, where it is not."""
+    return _NOTHING if index == torch._C._cuda_getDevice() else torch.cuda.device(index)
 
 
 def chunk_fwd(q, k, v, g, beta, S0=None, cu_seqlens=None, N: Optional[int] = None, o=None, S_T=None,
@@ -140,11 +170,13 @@ def chunk_fwd(q, k, v, g, beta, S0=None, cu_seqlens=None, N: Optional[int] = Non
         S_T = torch.empty((N, H, dv, dk), dtype=torch.float32, device=q.device)
     dt = _DTYPE.get(q.dtype, 99)
     need = int(lib.gdn_chunk_fwd_workspace_size(N, T_tot, H, dk, dv, dt))
-    ws = workspace if workspace is not None else _workspace(need, q.device)
-    _check(lib.gdn_chunk_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(S0), _ptr(cu_seqlens),
-                             N, T_tot, H, dk, dv, dt, _ptr(o), _ptr(S_T), _ptr(ws), ws.numel(), _stream()))
-    if check:
-        _check(lib.gdn_chunk_fwd_check(_ptr(ws), ws.numel(), _stream()))
+    index = q.get_device()
+    with _on(index):
+        stream, ws, ws_bytes = _stream_and_ws(index, need, workspace)
+        _check(lib.gdn_chunk_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(S0), _ptr(cu_seqlens),
+                                 N, T_tot, H, dk, dv, dt, _ptr(o), _ptr(S_T), ws.data_ptr(), ws_bytes, stream))
+        if check:
+            _check(lib.gdn_chunk_fwd_check(ws.data_ptr(), ws_bytes, stream))
     return o, S_T
 
 
@@ -167,11 +199,13 @@ def chunk_fwd_raw(q_raw, k_raw, v, a, b, S0=None, cu_seqlens=None, N: Optional[i
         S_T = torch.empty((N, H, dv, dk), dtype=torch.float32, device=q_raw.device)
     dt = _DTYPE.get(q_raw.dtype, 99)
     need = int(lib.gdn_chunk_fwd_workspace_size(N, T_tot, H, dk, dv, dt))
-    ws = workspace if workspace is not None else _workspace(need, q_raw.device)
-    _check(lib.gdn_chunk_fwd_raw(_ptr(q_raw), _ptr(k_raw), _ptr(v), _ptr(a), _ptr(b), _ptr(S0), _ptr(cu_seqlens),
-                                 N, T_tot, H, dk, dv, dt, _ptr(o), _ptr(S_T), _ptr(ws), ws.numel(), _stream()))
-    if check:
-        _check(lib.gdn_chunk_fwd_check(_ptr(ws), ws.numel(), _stream()))
+    index = q_raw.get_device()
+    with _on(index):
+        stream, ws, ws_bytes = _stream_and_ws(index, need, workspace)
+        _check(lib.gdn_chunk_fwd_raw(_ptr(q_raw), _ptr(k_raw), _ptr(v), _ptr(a), _ptr(b), _ptr(S0), _ptr(cu_seqlens),
+                                     N, T_tot, H, dk, dv, dt, _ptr(o), _ptr(S_T), ws.data_ptr(), ws_bytes, stream))
+        if check:
+            _check(lib.gdn_chunk_fwd_check(ws.data_ptr(), ws_bytes, stream))
     return o, S_T
 
 
@@ -203,11 +237,13 @@ def proj_w8(x, w, scale, H: int, dk: int, dv: int, out=None, workspace=None, che
                torch.empty((T, H), dtype=torch.float32, device=dev),
                torch.empty((T, H), dtype=torch.float32, device=dev))
     _need_cuda(*out)
-    ws = workspace if workspace is not None else _workspace(256, dev)
-    _check(lib.gdn_proj_w8(_ptr(x), _ptr(w), _ptr(scale), T, D, H, dk, dv, *[_ptr(t) for t in out], _ptr(ws),
-                           ws.numel(), _stream()))
-    if check:
-        _check(lib.gdn_chunk_fwd_check(_ptr(ws), ws.numel(), _stream()))
+    index = x.get_device()
+    with _on(index):
+        stream, ws, ws_bytes = _stream_and_ws(index, 256, workspace)
+        _check(lib.gdn_proj_w8(_ptr(x), _ptr(w), _ptr(scale), T, D, H, dk, dv, *[_ptr(t) for t in out], ws.data_ptr(),
+                               ws_bytes, stream))
+        if check:
+            _check(lib.gdn_chunk_fwd_check(ws.data_ptr(), ws_bytes, stream))
     return out
 
 
@@ -228,11 +264,13 @@ def attn_fwd(q, k, v, cu_seqlens=None, N: Optional[int] = None, max_len: Optiona
         max_len = T_tot // N
     if o is None:
         o = torch.empty_like(q)
-    ws = workspace if workspace is not None else _workspace(256, q.device)
-    _check(lib.gdn_attn_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(cu_seqlens), N, T_tot, H, d, max_len, float(scale),
-                            _DTYPE.get(q.dtype, 99), _ptr(o), _ptr(ws), ws.numel(), _stream()))
-    if check:
-        _check(lib.gdn_chunk_fwd_check(_ptr(ws), ws.numel(), _stream()))
+    index = q.get_device()
+    with _on(index):
+        stream, ws, ws_bytes = _stream_and_ws(index, 256, workspace)
+        _check(lib.gdn_attn_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(cu_seqlens), N, T_tot, H, d, max_len, float(scale),
+                                _DTYPE.get(q.dtype, 99), _ptr(o), ws.data_ptr(), ws_bytes, stream))
+        if check:
+            _check(lib.gdn_chunk_fwd_check(ws.data_ptr(), ws_bytes, stream))
     return o
 
 
@@ -271,41 +309,6 @@ def _index(name, t):
     if t.dim() != 3 or not t.is_cuda:
         _refuse(name, t, 0, t.dtype, (None, None, None))
     return t.get_device()
-
-
-def _stream_and_ws(index, nbytes, workspace):
-    """The current stream of a device, and a workspace: the caller's, or the cached one of this device, stream
-    and thread (the kernels of two threads' calls on one stream may take turns), or while a graph is being captured a
-    fresh one, so that the graph keeps memory of its own."""
-    stream = torch._C._cuda_getCurrentRawStream(index)
-    if workspace is None:
-        if torch._C._cuda_isCurrentStreamCapturing():
-            workspace = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=torch.device("cuda", index))
-        else:
-            key = (index, stream, get_ident())
-            workspace = _ws_cache.get(key)
-            if workspace is None or workspace.numel() < nbytes:
-                workspace = _ws_cache[key] = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=torch.device("cuda", index))
-        return stream, workspace, workspace.numel()
-    if not workspace.is_contiguous() or workspace.get_device() != index:
-        raise GdnError(6, "workspace must be a contiguous tensor on the inputs' device")
-    return stream, workspace, workspace.numel() * workspace.element_size()
-
-
-class _Nothing:
-    def __enter__(self):
-        return None
-
-    def __exit__(self, *exc):
-        return False
-
-
-_NOTHING = _Nothing()
-
-
-def _on(index):
-    """Makes the tensors' device the current one for a call, where it is not."""
-    return _NOTHING if index == torch._C._cuda_getDevice() else torch.cuda.device(index)
 
 
 _BF16, _I32, _FP32 = torch.bfloat16, torch.int32, torch.float32

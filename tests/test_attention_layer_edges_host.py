@@ -1,5 +1,10 @@
 """Host-side edges of the attention layer's entry points and of the binding's workspaces (no GPU needed)."""
+import contextlib
+import threading
+import types
+
 import pytest
+import torch
 
 
 @pytest.fixture(scope="module")
@@ -20,3 +25,95 @@ def test_injection_kinds_of_the_attention_layer(lib):
             assert lib.gdn_debug_inject(kind, 20000) == 2
     finally:
         assert lib.gdn_debug_inject(0, 0) == 0
+
+
+# ------------------------------------------------------------------ the binding's workspaces
+
+class Library:
+    """Takes every call and notes the address of its workspace."""
+
+    def __init__(self):
+        self.seen = []
+
+    def gdn_chunk_fwd_workspace_size(self, *args):
+        return 1024 * args[1]
+
+    def gdn_attn_decode_workspace_size(self, *args):
+        return 4096
+
+    def __getattr__(self, name):
+        def call(*args):
+            # the workspace stands before its size and the stream
+            self.seen.append((name, getattr(args[-3], "value", args[-3])))
+            return 0
+        return call
+
+
+@pytest.fixture
+def binding(monkeypatch):
+    """The binding on CPU tensors over a library that computes nothing, with a fake stream that may be capturing."""
+    from linear_attention_recurrent_chunked_b200 import gdn
+    lib, state = Library(), {"capturing": False}
+    monkeypatch.setattr(gdn, "load_library", lambda: lib)
+    monkeypatch.setattr(gdn, "_need_cuda", lambda *ts: None)
+    monkeypatch.setattr(gdn, "_on", lambda index: contextlib.nullcontext())
+    monkeypatch.setattr(gdn, "_index", lambda name, t: -1)
+    monkeypatch.setattr(gdn, "_bytes", lambda n, index: torch.empty(n, dtype=torch.uint8), raising=False)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: types.SimpleNamespace(cuda_stream=0x7001))
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda index: 0x7001)
+    monkeypatch.setattr(torch._C, "_cuda_isCurrentStreamCapturing", lambda: state["capturing"])
+    return gdn, lib, state
+
+
+def calls(gdn):
+    """Every entry point that takes a workspace, by name, for T tokens."""
+    def bf(*s):
+        return torch.zeros(s, dtype=torch.bfloat16)
+
+    def f32(*s):
+        return torch.zeros(s)
+
+    def i32(*s):
+        return torch.zeros(s, dtype=torch.int32)
+
+    return {
+        "chunk_fwd": lambda T: gdn.chunk_fwd(bf(T, 2, 128), bf(T, 2, 128), bf(T, 2, 128), f32(T, 2), f32(T, 2)),
+        "chunk_fwd_raw": lambda T: gdn.chunk_fwd_raw(bf(T, 2, 128), bf(T, 2, 128), bf(T, 2, 128), f32(T, 2), f32(T, 2)),
+        "proj_w8": lambda T: gdn.proj_w8(bf(T, 64), torch.zeros((26, 64), dtype=torch.int8), f32(26), 1, 8, 8),
+        "attn_fwd": lambda T: gdn.attn_fwd(bf(T, 2, 128), bf(T, 2, 128), bf(T, 2, 128)),
+        "qk_norm_rope": lambda T: gdn.qk_norm_rope(bf(T, 2, 64), bf(T, 2, 64), None, None, i32(T)),
+        "attn_prefill": lambda T: gdn.attn_prefill(bf(T, 2, 64), bf(T, 2, 64), bf(T, 2, 64)),
+        "attn_decode": lambda T: gdn.attn_decode(bf(T, 2, 64), bf(3, 2, 16, 64), bf(3, 2, 16, 64), i32(T, 1), i32(T)),
+    }
+
+
+NAMES = ["chunk_fwd", "chunk_fwd_raw", "proj_w8", "attn_fwd", "qk_norm_rope", "attn_prefill", "attn_decode"]
+
+
+@pytest.mark.parametrize("name", NAMES)
+def test_a_captured_call_keeps_a_workspace_of_its_own(binding, name):
+    """A graph's workspace is not the cached one, which a later, larger call replaces and frees."""
+    gdn, lib, state = binding
+    call = calls(gdn)[name]
+    call(64)
+    call(64)
+    cached = lib.seen[0][1]
+    assert cached and lib.seen[1][1] == cached  # eager calls of one thread and stream share theirs
+    state["capturing"] = True
+    call(64)
+    assert lib.seen[2][1] != cached
+    state["capturing"] = False
+    call(64)
+    assert lib.seen[3][1] == cached
+
+
+@pytest.mark.parametrize("name", NAMES)
+def test_two_threads_on_one_stream_have_workspaces_of_their_own(binding, name):
+    """Their calls' kernels may take turns on the stream."""
+    gdn, lib, _ = binding
+    call = calls(gdn)[name]
+    call(64)
+    t = threading.Thread(target=call, args=(64,))
+    t.start()
+    t.join()
+    assert len(lib.seen) == 2 and lib.seen[0][1] != lib.seen[1][1]
