@@ -9,7 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
-from threading import get_ident
+import threading
 from typing import Optional
 
 import torch
@@ -108,7 +108,7 @@ def chunk_fwd_workspace_size(N: int, T_tot: int, H: int, dk: int, dv: int, dtype
     return int(load_library().gdn_chunk_fwd_workspace_size(N, T_tot, H, dk, dv, _DTYPE[dtype]))
 
 
-_ws_cache = {}
+_cached = threading.local()  # each thread's workspaces, which end with it
 
 
 def _bytes(n, index):
@@ -124,10 +124,10 @@ def _stream_and_ws(index, nbytes, workspace):
         if torch._C._cuda_isCurrentStreamCapturing():
             workspace = _bytes(max(nbytes, 256), index)
         else:
-            key = (index, stream, get_ident())
-            workspace = _ws_cache.get(key)
+            mine, key = _cached.__dict__, (index, stream)
+            workspace = mine.get(key)
             if workspace is None or workspace.numel() < nbytes:
-                workspace = _ws_cache[key] = _bytes(max(nbytes, 256), index)
+                workspace = mine[key] = _bytes(max(nbytes, 256), index)
         return stream, workspace, workspace.numel()
     if not workspace.is_contiguous() or workspace.get_device() != index:
         raise GdnError(6, "workspace must be a contiguous tensor on the inputs' device")

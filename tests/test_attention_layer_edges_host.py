@@ -1,7 +1,9 @@
 """Host-side edges of the attention layer's entry points and of the binding's workspaces (no GPU needed)."""
 import contextlib
+import gc
 import threading
 import types
+import weakref
 
 import pytest
 import torch
@@ -117,3 +119,35 @@ def test_two_threads_on_one_stream_have_workspaces_of_their_own(binding, name):
     t.start()
     t.join()
     assert len(lib.seen) == 2 and lib.seen[0][1] != lib.seen[1][1]
+
+
+@pytest.mark.parametrize("name", NAMES)
+def test_workspaces_of_a_thread_end_with_it(binding, name, monkeypatch):
+    """A server that starts threads does not gather their workspaces; its own stays."""
+    gdn, lib, _ = binding
+    made = []
+
+    def make(n, index):
+        t = torch.empty(n, dtype=torch.uint8)
+        made.append(weakref.ref(t))
+        return t
+
+    monkeypatch.setattr(gdn, "_bytes", make)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda index: 0x7100 + NAMES.index(name))  # unused so far
+    call, together = calls(gdn)[name], threading.Barrier(5)
+
+    def serve():
+        together.wait()
+        call(64)
+        together.wait()
+
+    call(64)
+    threads = [threading.Thread(target=serve) for _ in range(5)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    gc.collect()
+    assert [r() is not None for r in made] == [True] + [False] * 5
+    call(64)
+    assert lib.seen[-1][1] == lib.seen[0][1]
