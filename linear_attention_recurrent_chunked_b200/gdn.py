@@ -345,6 +345,8 @@ def qk_norm_rope(q, k, wq, wk, positions, v=None, rot: Optional[int] = None, bas
         pkc = _flat("k_cache", k_cache, index, dtype, shape)
         pvc = _flat("v_cache", v_cache, index, dtype, shape)
         ps = _flat("slots", slots, index, _I32, (T,))
+    elif k_cache is not None or v_cache is not None:
+        raise GdnError(1, "k_cache and v_cache need slots")
     pwq = None if wq is None else _flat("wq", wq, index, _FP32, (d,))
     pwk = None if wk is None else _flat("wk", wk, index, _FP32, (d,))
     pp = None if positions is None else _flat("positions", positions, index, _I32, (T,))

@@ -151,3 +151,16 @@ def test_workspaces_of_a_thread_end_with_it(binding, name, monkeypatch):
     assert [r() is not None for r in made] == [True] + [False] * 5
     call(64)
     assert lib.seen[-1][1] == lib.seen[0][1]
+
+
+# ------------------------------------------------------------------ arguments
+
+@pytest.mark.parametrize("which", [("k_cache",), ("v_cache",), ("k_cache", "v_cache")])
+def test_caches_without_slots_are_refused(binding, which):
+    """As the C entry point does: the cache would stay as it was, without a word."""
+    gdn, lib, _ = binding
+    x = torch.zeros((4, 2, 64), dtype=torch.bfloat16)
+    cache = torch.zeros((3, 2, 16, 64), dtype=torch.bfloat16)
+    with pytest.raises(gdn.GdnError) as e:
+        gdn.qk_norm_rope(x, x, None, None, torch.zeros(4, dtype=torch.int32), v=x, **dict.fromkeys(which, cache))
+    assert e.value.status == 1 and not lib.seen
