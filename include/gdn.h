@@ -340,10 +340,10 @@ gdn_status gdn_attn_prefill(const void *q, int64_t q_stride, const void *k, int6
  *     o_b = sum_j softmax_j(scale * q_b . k_j) v_j
  * with j over the prefix_len keys of the prefix and the lens[b] keys of sequence b (its new token's
  * among them, where gdn_qk_norm_rope has put it). No key is masked otherwise.
- *   q, o         [B][Hq][d] bf16, contiguous; o must not alias the inputs
+ *   q, o         [B][Hq][d] bf16, contiguous, B >= 1; o must not alias the inputs
  *   page_table   [B][max_pages] int32: key t of sequence b is in page page_table[b][t / page_size] at
  *                place t % page_size. Entries past the last key's page are not read; a page may stand
- *                in several rows or several times. max_pages page_size <= 2^30,
+ *                in several rows or several times. max_pages >= 1, max_pages page_size <= 2^30,
  *                and B Hkv max_pages page_size below 2^35 (the work is counted in steps of 16 keys).
  *   lens         [B] int32, from 0 to max_pages page_size. With no key at all a sequence's o is zero.
  *   prefix_pages [ceil(prefix_len / page_size)] int32 on the device, or NULL when prefix_len is 0. The

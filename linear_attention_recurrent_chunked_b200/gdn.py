@@ -416,7 +416,8 @@ def attn_decode(q, k_cache, v_cache, page_table, lens, prefix_pages=None, prefix
                 workspace=None, check: bool = False):
     """Attention of one new token per sequence over the paged cache (see include/gdn.h): q [B,Hq,d]
     bf16, k_cache, v_cache [pages,Hkv,page_size,d] bf16, page_table [B,max_pages] int32, lens [B] int32;
-    prefix_pages [n] int32 and prefix_len: a prefix that all sequences share. Returns o [B,Hq,d]."""
+    prefix_pages [n] int32 and prefix_len: a prefix that all sequences share. B and max_pages may be 0 here.
+    Returns o [B,Hq,d]."""
     lib = load_library()
     if q.dtype is not _BF16:
         raise GdnError(3, "q is %s, not %s" % (q.dtype, _BF16))
@@ -453,8 +454,14 @@ def attn_decode(q, k_cache, v_cache, page_table, lens, prefix_pages=None, prefix
             po = o.data_ptr()
         else:
             po = _flat("o", o, index, _BF16, (B, Hq, d))
+        if not B:
+            return o
+        columns = table[1]
+        if not columns:  # the library wants one: of no page
+            page_table, columns = page_table.new_full((B, 1), -1), 1
+            pt = page_table.data_ptr()
         stream, ws, ws_bytes = _stream_and_ws(index, lib.gdn_attn_decode_workspace_size(B, Hq, Hkv, d, prefix_len), workspace)
-        _check(lib.gdn_attn_decode(pq, pk, pv, pages, page_size, pt, table[1], pl, pp, prefix_len, B, Hq, Hkv, d, scale,
+        _check(lib.gdn_attn_decode(pq, pk, pv, pages, page_size, pt, columns, pl, pp, prefix_len, B, Hq, Hkv, d, scale,
                                    GDN_BF16, po, ws.data_ptr(), ws_bytes, stream))
         if check:
             _check(lib.gdn_chunk_fwd_check(ws.data_ptr(), ws_bytes, stream))

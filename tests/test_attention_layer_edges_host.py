@@ -164,3 +164,19 @@ def test_caches_without_slots_are_refused(binding, which):
     with pytest.raises(gdn.GdnError) as e:
         gdn.qk_norm_rope(x, x, None, None, torch.zeros(4, dtype=torch.int32), v=x, **dict.fromkeys(which, cache))
     assert e.value.status == 1 and not lib.seen
+
+
+def test_decode_of_no_sequences(binding):
+    """An empty batch, as the other operators take no tokens: an empty output, nothing launched; its arguments are
+    still checked."""
+    gdn, lib, _ = binding
+    bf, i32 = torch.bfloat16, torch.int32
+    cache = torch.zeros((3, 2, 16, 64), dtype=bf)
+    args = dict(q=torch.zeros((0, 4, 64), dtype=bf), k_cache=cache, v_cache=cache, page_table=torch.zeros((0, 5), dtype=i32),
+                lens=torch.zeros(0, dtype=i32))
+    assert gdn.attn_decode(**args, check=True).shape == (0, 4, 64) and not lib.seen
+    o = torch.zeros((0, 4, 64), dtype=bf)
+    assert gdn.attn_decode(**args, o=o) is o and not lib.seen
+    with pytest.raises(gdn.GdnError) as e:
+        gdn.attn_decode(**dict(args, lens=torch.zeros(1, dtype=i32)))
+    assert e.value.status == 2

@@ -145,3 +145,20 @@ def test_decode_wait_that_runs_out(Hq, Hkv, prefix, d, kind):
     n = 128 // (Hq // Hkv) if prefix else 2
     assert torch.equal(o[n:], want[n:]) and torch.equal(o[2:, Hq // Hkv:], want[2:, Hq // Hkv:])
     assert torch.equal(gdn.attn_decode(**w, check=True), want)
+
+
+# ------------------------------------------------------------------ nothing of its own
+
+@pytest.mark.parametrize("prefix", [0, 100])
+def test_decode_page_table_without_columns(prefix):
+    """A batch none of whose sequences has a page yet: the prefix alone, or zeros; a length that says otherwise is
+    reported. And a batch of no sequences at all."""
+    gen = torch.Generator().manual_seed(70)
+    w = cached(gen, [0] * 5, 8, 2, 64, 16, prefix)
+    w["page_table"] = w["page_table"][:, :0].contiguous()
+    check_decode(w)
+    with pytest.raises(gdn.GdnError) as e:
+        gdn.attn_decode(**on_gpu(dict(w, lens=w["lens"] + 3)), check=True)
+    assert e.value.status == 10
+    none = dict(w, q=w["q"][:0], page_table=w["page_table"][:0], lens=w["lens"][:0])
+    assert gdn.attn_decode(**on_gpu(none), check=True).shape == (0, 8, 64)
