@@ -162,3 +162,20 @@ def test_decode_page_table_without_columns(prefix):
     assert e.value.status == 10
     none = dict(w, q=w["q"][:0], page_table=w["page_table"][:0], lens=w["lens"][:0])
     assert gdn.attn_decode(**on_gpu(none), check=True).shape == (0, 8, 64)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("prefix", [0, 70])
+@pytest.mark.parametrize("at", [[0], [2999], [0, 2999], [5, 6, 37, 38, 70, 1500], [31, 32, 63, 64, 96]])
+def test_decode_few_sequences_with_keys_among_many_without(at, prefix, d):
+    """Runs of a warp that cross stretches of empty sequences, of less and more than 32, up to the batch's end."""
+    lens = [0] * 3000
+    for i, b in enumerate(at):
+        lens[b] = 1200 + 17 * i
+    w = cached(torch.Generator().manual_seed(71 + len(at)), lens, 2, 1, d, 16, prefix)
+    o = gdn.attn_decode(**on_gpu(w), check=True)
+    some = sorted({0, 1, 33, 2998, 2999, *at})
+    check_decode(dict(w, q=w["q"][some], page_table=w["page_table"][some], lens=w["lens"][some]), got=o[some])
+    if not prefix:
+        empty = torch.tensor([n == 0 for n in lens])
+        assert (o[empty.cuda()] == 0).all()
