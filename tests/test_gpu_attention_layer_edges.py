@@ -7,7 +7,7 @@ import torch
 
 from oracle import attention_layer as al
 from linear_attention_recurrent_chunked_b200 import gdn
-from tests.test_gpu_attention_layer import attn_tol, cached, check_decode, close, on_gpu, prompt
+from tests.test_gpu_attention_layer import BF, attn_tol, cached, check_decode, close, on_gpu, prompt
 
 pytestmark = pytest.mark.gpu
 INF = float("inf")
@@ -179,3 +179,46 @@ def test_decode_few_sequences_with_keys_among_many_without(at, prefix, d):
     if not prefix:
         empty = torch.tensor([n == 0 for n in lens])
         assert (o[empty.cuda()] == 0).all()
+
+
+# ------------------------------------------------------------------ packs
+
+@pytest.mark.parametrize("lens,Hq,Hkv", [([70, 90, 200], 4, 2), ([33], 3, 1), ([900] + [3] * 40, 8, 2), ([0, 0], 4, 2)])
+def test_prefill_rows_around_the_output_stay(lens, Hq, Hkv):
+    """An output inside a larger buffer: the rows before it and those behind the last sequence stay as they were."""
+    gen = torch.Generator().manual_seed(90)
+    T, d = sum(lens), 64
+    q, k, v, cu = (x.cuda() for x in prompt(gen, lens, Hq, Hkv, d))
+    v = v[:, Hq + Hkv:]
+    buffer = torch.full((T + 300, Hq, d), 3.0, dtype=BF, device="cuda")
+    o = gdn.attn_prefill(q, k, v, cu, max_len=max(lens), o=buffer[150:150 + T], check=True)
+    assert (buffer[:150] == 3.0).all() and (buffer[150 + T:] == 3.0).all()
+    ref, a = al.prompt_attention(q.cpu(), k.cpu(), v.cpu(), lens)
+    close(o, ref, attn_tol(ref, a, q, k, d, max(lens)))
+
+
+@pytest.mark.parametrize("N", [223, 224, 225, 448, 449])
+def test_prefill_sequence_counts_around_the_threads(N):
+    """Packs numbered sequence by sequence, with one sequence for each thread that counts the tiles, one less and one
+    more; and the same with two."""
+    gen = torch.Generator().manual_seed(N)
+    lens = torch.randint(0, 40, (N,), generator=gen).tolist()
+    lens[0], lens[N // 2], lens[-1] = 0, 700, 1
+    q, k, v, cu = prompt(gen, lens, 4, 2, 64)
+    v = v[:, 6:].contiguous()
+    o = gdn.attn_prefill(q.cuda(), k.cuda(), v.cuda(), cu.cuda(), max_len=700, check=True)
+    ref, a = al.prompt_attention(q, k, v, lens)
+    close(o, ref, attn_tol(ref, a, q, k, 64, 700))
+
+
+@pytest.mark.parametrize("lens,Hkv,most", [([100] + [5] * 28 + [64], 2, m) for m in (100, 128, 129, 160, 304)] +
+                         [([64] * 10, 8, m) for m in (64, 96, 128, 129, 640)])
+def test_prefill_both_numberings_of_a_pack(lens, Hkv, most):
+    """The bound on the lengths decides how blocks are numbered, between 128 and 129 in both packs (tiles of 32 positions: in
+    the first the blocks then outnumber those that run at once, in the second they exceed the tiles by more than half).
+    The outputs do not depend on it, bit for bit, and are those of each sequence alone."""
+    gen = torch.Generator().manual_seed(91)
+    q, k, v, cu = (x.cuda() for x in prompt(gen, lens, 4 * Hkv, Hkv, 128))
+    v = v[:, 5 * Hkv:]
+    want = torch.cat([gdn.attn_prefill(x, y, z, check=True) for x, y, z in zip(*(t.split(lens) for t in (q, k, v)))])
+    assert torch.equal(gdn.attn_prefill(q, k, v, cu, max_len=most, check=True), want)
