@@ -295,7 +295,8 @@ gdn_status gdn_attn_fwd(const void *q, const void *k, const void *v, const int32
  *     x^ = x w / sqrt(mean(x^2) + eps)
  *     y_i = x^_i cos a_i - x^_{i+rot/2} sin a_i,  y_{i+rot/2} = x^_{i+rot/2} cos a_i + x^_i sin a_i
  *         for i < rot/2, with a_i = positions[t] base^(-2i/rot);   y_i = x^_i for i >= rot
- * in fp32 (angles in fp64 turns, so that far positions keep their phase), rounded once.
+ * in fp32, rounded once. The angle is taken from a 64-bit fraction of a turn and is within 2e-7 radians at any
+ * position.
  *   q, k, v   dtype, with strides; v is read only with slots
  *   wq, wk    [d] fp32 norm weights, or NULL for ones; eps >= 0
  *   positions [T] int32 (may be NULL when rot is 0)

@@ -8,9 +8,11 @@
 //     y_{i+r/2} = x^_{i+r/2} cos(a_i) + x^_i sin(a_i)        elements from r on: y = x^
 //
 // all in fp32 and rounded once, when y is stored. The angle is formed in turns, pos f_i with f_i =
-// base^(-2i/r) / (2 pi), as a 64-bit binary fraction that wraps by itself: pos times round(2^64 f_i)
-// modulo 2^64 is off by at most 2^-34 turns at any int32 position, where an fp32 product would be off by
-// 0.06 radians at position 10^6 already. The fraction's upper 32 bits are then a signed fp32 value.
+// base^(-2i/r) / (2 pi), as a 64-bit binary fraction that wraps by itself: pos times 2^64 f_i modulo 2^64.
+// The frequencies come from a chain of up to 63 rounded products, which puts 2^64 f_i off by 30 at most (up to 3.7
+// found, for bases near 1), 2^-28 turns at any int32 position, where an fp32 product would be off by 0.06 radians at
+// position 10^6 already. The fraction's upper 32 bits, 2^-32 less at most, then become a signed fp32 value within
+// 2^-26: together less than 2^-25 turns, 2e-7 radians.
 //
 // Bound: HBM (each row is read once and written once), as long as few enough instructions are spent on
 // an element. A lane holds two 16-byte runs of a row: a run of first elements of pairs and the run of their
@@ -279,7 +281,7 @@ cudaError_t launch(const NormRope &a, cudaStream_t st) {
     while (a.slots && (1 << p.page_log) < a.page_size) ++p.page_log;
     p.warps = std::min<int64_t>((int64_t)a.T * (p.gq + p.gk + p.gv), (148 * kResident - 1) * kWarps);  // one CTA checks
     Freq fr;
-    // (extended precision throughout: the chain of products then costs nothing in the 64 bits)
+    // (extended precision throughout; what the chain of products loses is said above)
     const long double step = a.rot ? powl(a.base, -2.0L / a.rot) : 1.0L;
     long double f = 0x1p64L / 6.283185307179586476925287L;
     for (int i = 0; i < a.rot / 2; ++i, f *= step) fr.f[i] = (uint64_t)(f + 0.5L);

@@ -7,7 +7,7 @@ import torch
 
 from oracle import attention_layer as al
 from linear_attention_recurrent_chunked_b200 import gdn
-from tests.test_gpu_attention_layer import BF, attn_tol, cached, check_decode, close, on_gpu, prompt
+from tests.test_gpu_attention_layer import BF, attn_tol, cached, check_decode, close, on_gpu, prompt, randn, rope_tol
 
 pytestmark = pytest.mark.gpu
 INF = float("inf")
@@ -222,3 +222,21 @@ def test_prefill_both_numberings_of_a_pack(lens, Hkv, most):
     v = v[:, 5 * Hkv:]
     want = torch.cat([gdn.attn_prefill(x, y, z, check=True) for x, y, z in zip(*(t.split(lens) for t in (q, k, v)))])
     assert torch.equal(gdn.attn_prefill(q, k, v, cu, max_len=most, check=True), want)
+
+
+# ------------------------------------------------------------------ angles
+
+@pytest.mark.parametrize("dtype", [BF, torch.float32])
+@pytest.mark.parametrize("base", [1.01, 500.0, 1e12])
+@pytest.mark.parametrize("d,rot", [(128, 128), (64, 64), (128, 16)])
+def test_norm_rope_ends_of_the_positions(d, rot, base, dtype):
+    """The first and last int32 positions and others far out, where the frequencies of a base near 1 all count. (The kernel's
+    angle is within 2e-7 of the formula's, the fp64 oracle's within 2^31 2^-51 = 1e-6: 3 and 16 fp32 half steps of the 32 that
+    rope_tol allows for angle, sine, cosine and products.)"""
+    gen = torch.Generator().manual_seed(92)
+    pos = torch.tensor([2 ** 31 - 1, -2 ** 31, 0, -1, 10 ** 9 + 7, 2 ** 30, 1], dtype=torch.int32)
+    x = randn(gen, len(pos), 3, d, dtype=dtype)
+    y, b = al.norm_rope(x, None, pos, rot, base=base)
+    q, k = gdn.qk_norm_rope(x.cuda(), x[:, :1].contiguous().cuda(), None, None, pos.cuda(), rot=rot, base=base, check=True)
+    close(q, y, rope_tol(y, b, d, dtype))
+    close(k, y[:, :1], rope_tol(y, b, d, dtype)[:, :1])
