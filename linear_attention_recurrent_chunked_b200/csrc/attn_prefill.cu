@@ -23,9 +23,9 @@
 // Weights have their own tensor memory beside S, so that the next S does not wait for O += P V; with O that
 // is 224 of the CTA's 256 columns, and the last 32 hold 64 of Q's columns: those products of S take one operand
 // from shared memory instead of two (32 cycles of 128x64x16 against 48 at 128 bytes a cycle).
-// Bound: tensor pipe and power. One sequence of 10,240 tokens, 16/4 heads, d = 128: 345 us in short runs, 373 over
-// seconds, at 1,000 W and 1.52 GHz: 1,245 and 1,150 TFLOP/s, against 1,656 and 1,470 of a library bf16 product of the same
-// machine. A step then takes 812 cycles of an SM, of which its products need 576 (8 of 128x64x16, 4 of 128x128x16).
+// Bound: tensor pipe and power. One sequence of 10,240 tokens, 16/4 heads, d = 128: 345 us in short runs, 400 over
+// seconds, at 990 W and 1.50 GHz: 1,245 and 1,075 TFLOP/s, against 1,656 and 1,385 of a library bf16 product of the same
+// kind of machine. A step then takes 812 cycles of an SM, of which its products need 576 (8 of 128x64x16, 4 of 128x128x16).
 // At 4,096 tokens: 68.4 us, exponentials (MUFU) 57 %, issue slots 38 %. The same long prompt on the way here, in short
 // runs: two tiles in one CTA, whose softmax warps fall into lockstep, 361 us (with two threads per row 403, with steps
 // of 128 keys, where P lies over S, 391); one tile per CTA 349, with a quarter of the exponentials as polynomials on
