@@ -54,8 +54,8 @@ __device__ __noinline__ inline void drain_bar(uint64_t *bar, uint32_t parity, co
 
 // Every kernel here is launched to start while the one before it in the stream drains (launch_early): it sets
 // up what is its own, then waits here for that one's end before it touches global memory. Two read some of their inputs
-// before: the decode kernel behind a prefix, and the joining kernel (its lengths and pages). They start once every CTA of
-// the kernel before them has passed this wait itself, so what stood before that one, which wrote those inputs, has ended.
+// before: the decode kernel behind a prefix, and the joining kernel (its lengths and pages). They start only after every
+// CTA of their call's first kernel has passed this wait, so whatever wrote those inputs before the call has ended.
 __device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 // The next kernel may start. (Its own wait still waits for this kernel's end.)
 __device__ __forceinline__ void grid_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
