@@ -240,3 +240,45 @@ def test_norm_rope_ends_of_the_positions(d, rot, base, dtype):
     q, k = gdn.qk_norm_rope(x.cuda(), x[:, :1].contiguous().cuda(), None, None, pos.cuda(), rot=rot, base=base, check=True)
     close(q, y, rope_tol(y, b, d, dtype))
     close(k, y[:, :1], rope_tol(y, b, d, dtype)[:, :1])
+
+
+# ------------------------------------------------------------------ a cache of more than 2^32 elements
+
+def test_cache_beyond_32_bits():
+    """Pages on both sides of element 2^31 and 2^32 of the cache (9 GB each for keys and values), written by the norms'
+    kernel and read as own keys and as a shared prefix; what stands in the other slots of these pages stays."""
+    Hq, Hkv, d, page = 8, 4, 128, 64
+    size = Hkv * page * d
+    pages = 2 ** 32 // size + 40
+    at = [3, 2 ** 31 // size - 1, 2 ** 31 // size, 2 ** 32 // size - 1, 2 ** 32 // size, pages - 1]
+    gen = torch.Generator().manual_seed(93)
+    kc, vc = (torch.empty((pages, Hkv, page, d), dtype=BF, device="cuda") for _ in range(2))
+    for c in (kc, vc):
+        for p in at:
+            c[p] = 5.0
+    # every page but two gets 50 tokens of its own sequence; those two 64 and 6 of a prefix
+    own, prefix = [at[0], at[1], at[2], at[5]], [at[4], at[3]]
+    slots = torch.tensor([p * page + t for p in own for t in range(50)] + [prefix[0] * page + t for t in range(64)] +
+                         [prefix[1] * page + t for t in range(6)], dtype=torch.int32).cuda()
+    T = len(slots)
+    x = randn(gen, T, Hq + 2 * Hkv, d).cuda()
+    pos = torch.arange(T, dtype=torch.int32).cuda()
+    q, k = gdn.qk_norm_rope(x[:, :Hq], x[:, Hq:Hq + Hkv], None, None, pos, v=x[:, Hq + Hkv:], k_cache=kc, v_cache=vc, slots=slots,
+                            check=True)
+    small = {p: i for i, p in enumerate(at)}  # the same pages in a cache of their own
+    for c, want in ((kc, k), (vc, x[:, Hq + Hkv:])):
+        got = torch.stack([c[p] for p in at])
+        expect = torch.full_like(got, 5.0)
+        for t, s in enumerate(slots.tolist()):
+            expect[small[s // page], :, s % page] = want[t]
+        assert torch.equal(got, expect)
+    lens, i32 = [50, 33, 1, 50], torch.int32
+    args = dict(q=q[:4].contiguous(), lens=torch.tensor(lens, dtype=i32).cuda(), prefix_len=70)
+    big = dict(k_cache=kc, v_cache=vc, page_table=torch.tensor(own, dtype=i32).view(4, 1).cuda(),
+               prefix_pages=torch.tensor(prefix, dtype=i32).cuda())
+    near = dict(k_cache=torch.stack([kc[p] for p in at]), v_cache=torch.stack([vc[p] for p in at]),
+                page_table=torch.tensor([small[p] for p in own], dtype=i32).view(4, 1).cuda(),
+                prefix_pages=torch.tensor([small[p] for p in prefix], dtype=i32).cuda())
+    o = gdn.attn_decode(**args, **big, check=True)
+    assert torch.equal(o, gdn.attn_decode(**args, **near, check=True))
+    check_decode({n: (y.cpu() if hasattr(y, "cpu") else y) for n, y in {**args, **near}.items()}, got=o)
